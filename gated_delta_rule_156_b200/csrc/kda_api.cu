@@ -9,6 +9,7 @@
 
 #include "../../include/kda.h"
 #include "kda_internal.h"
+#include "kda_layer_internal.h"
 
 namespace {
 
@@ -214,6 +215,15 @@ void* noalloc_scratch(cudaError_t* err) {
 }
 
 }  // namespace
+
+namespace kda {
+
+cudaError_t api_take_workspace(size_t bytes, cudaStream_t stream, void** ws) {
+  return take_workspace(bytes, stream, ws);
+}
+void api_record_cuda_error(cudaError_t e) { (void)cuda_fail(e); }
+
+}  // namespace kda
 
 extern "C" {
 

@@ -1,0 +1,448 @@
+// Short causal convolution: forward, backward and the step for new tokens.
+//
+//   pre_t = bias + sum_j w_j x_{t-(W-1)+j},   out_t = act(pre_t)
+// per channel, with x at the W - 1 places before a sequence taken from its
+// initial state.  W is 2, 3 or 4, so an element costs 2 W flops and an
+// activation against 2 * sizeof(io) bytes: the kernels are bound by HBM.
+//
+// Work split: a thread owns VEC neighbouring channels (one 16-byte access a
+// token in the forward) and a run of consecutive tokens, over which the last
+// W - 1 inputs stay in registers.  The run's first W - 1 inputs are read by
+// the run before it as well; those reads come out of L2.
+#include "kda_layer.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kUnroll = 4;  // token loads in flight per thread
+
+template <typename IO, int W, int VEC>
+struct Taps {
+  float w[W][VEC], b[VEC];
+  __device__ __forceinline__ void load(const ConvArgs& a, int c0) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = a.weight[(size_t)(c0 + i) * W + j];
+      b[i] = a.bias ? a.bias[c0 + i] : 0.f;
+    }
+  }
+};
+
+// Input at position t of a sequence (t >= start - (W-1)): x, or the past.
+template <typename IO, int W, int VEC>
+__device__ __forceinline__ void input_at(const ConvArgs& a, const SeqCursor& q, int t,
+                                         int c0, float (&v)[VEC]) {
+  if (t >= q.start) {
+    load_vec<IO, VEC>(static_cast<const IO*>(a.x) + (int64_t)t * a.x_stride + c0, v);
+  } else if (a.past) {
+    const int64_t row = (int64_t)q.s * (W - 1) + (t - q.start + W - 1);
+    load_vec<IO, VEC>(static_cast<const IO*>(a.past) + row * a.D + c0, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+  }
+}
+
+__device__ __forceinline__ float act_f(float x, int act) {
+  return act == kActSilu ? x * sigmoid_f(x) : x;
+}
+__device__ __forceinline__ float act_grad(float x, int act) {
+  return act == kActSilu ? silu_grad(x, sigmoid_f(x)) : 1.f;
+}
+
+template <typename IO, int W, int VEC>
+__device__ __forceinline__ void taps_dot(const Taps<IO, W, VEC>& k,
+                                         const float (&win)[W - 1][VEC],
+                                         const float (&x)[VEC], float (&pre)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float p = k.b[i];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][i], win[j][i], p);
+    pre[i] = fmaf(k.w[W - 1][i], x[i], p);
+  }
+}
+
+template <int W, int VEC>
+__device__ __forceinline__ void slide(float (&win)[W - 1][VEC], const float (&x)[VEC]) {
+#pragma unroll
+  for (int j = 0; j + 1 < W - 1; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) win[j][i] = win[j + 1][i];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) win[W - 2][i] = x[i];
+}
+
+// Block (channel vectors, runs); the grid's runs go over all tokens, then
+// over the n_seqs * (W - 1) rows of the final states.
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(256)
+    conv_fwd_kernel(ConvArgs a, int nvec, int run, int64_t n_runs) {
+  const int cv = blockIdx.y * blockDim.x + threadIdx.x;
+  int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (cv >= nvec) return;
+  const int c0 = cv * VEC;
+  if (r >= n_runs) {  // final state row
+    r -= n_runs;
+    if (!a.final_state || r >= (int64_t)a.n_seqs * (W - 1)) return;
+    SeqCursor q;
+    q.s = (int)(r / (W - 1));
+    seq_range(a.cu, q.s, a.T, &q.start, &q.end);
+    float v[VEC];
+    input_at<IO, W, VEC>(a, q, q.end - (W - 1) + (int)(r % (W - 1)), c0, v);
+    store_vec<IO, VEC>(static_cast<IO*>(a.final_state) + r * a.D + c0, v);
+    return;
+  }
+  Taps<IO, W, VEC> k;
+  k.load(a, c0);
+  const IO* x = static_cast<const IO*>(a.x) + c0;
+  IO* out = static_cast<IO*>(a.out) + c0;
+  int64_t t = r * run;
+  const int64_t t1 = min(t + run, a.tokens);
+  while (t < t1) {
+    SeqCursor q;
+    if (!find_seq(a.cu, a.n_seqs, a.T, (int)t, &q)) return;
+    if (t < q.start) t = q.start;
+    const int64_t e = min((int64_t)q.end, t1);
+    if (t >= e) break;
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      input_at<IO, W, VEC>(a, q, (int)t - (W - 1) + j, c0, win[j]);
+    for (; t < e; t += kUnroll) {
+      Raw<IO, VEC> raw[kUnroll];
+      const int m = (int)min((int64_t)kUnroll, e - t);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+        if (i < m) raw[i] = load_raw<IO, VEC>(x + (t + i) * a.x_stride);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        if (i >= m) break;
+        float v[VEC], pre[VEC];
+        unpack(raw[i], v);
+        taps_dot<IO, W, VEC>(k, win, v, pre);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
+        store_vec<IO, VEC>(out + (t + i) * a.D, pre);
+        slide<W, VEC>(win, v);
+      }
+    }
+    t = e;
+  }
+}
+
+// Gradients.  dpre_t = d_out_t act'(pre_t) reaches dx at the W places
+// t-(W-1) .. t; the thread walks its run and W - 1 tokens further, carrying
+// the W - 1 unfinished dx in registers, and sums dw_j += dpre_t x_{t-(W-1)+j}
+// and db over the run itself.  The block's runs are summed in shared memory
+// in a fixed order; conv_weight_sum_kernel sums the blocks.  The rows of
+// d_initial_state are independent of the runs and have threads of their own.
+constexpr int kBwdLanes = 32, kBwdRuns = 8;
+
+template <typename IO, int W, int VEC>
+__device__ void past_grad(const ConvArgs& a, const Taps<IO, W, VEC>& k, int64_t row,
+                          int c0) {
+  SeqCursor q;
+  q.s = (int)(row / (W - 1));
+  const int r = (int)(row % (W - 1));
+  seq_range(a.cu, q.s, a.T, &q.start, &q.end);
+  const int len = q.end - q.start;
+  float g[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) g[i] = 0.f;
+  // row r of the past is input r-(W-1); token tau <= r reads it with tap r-tau
+  for (int tau = 0; tau <= r && tau < len; ++tau) {
+    float win[W - 1][VEC], x[VEC], pre[VEC], dy[VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      input_at<IO, W, VEC>(a, q, q.start + tau - (W - 1) + j, c0, win[j]);
+    input_at<IO, W, VEC>(a, q, q.start + tau, c0, x);
+    taps_dot<IO, W, VEC>(k, win, x, pre);
+    load_vec<IO, VEC>(static_cast<const IO*>(a.d_out) + (int64_t)(q.start + tau) * a.D + c0,
+                      dy);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (j == r - tau)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          g[i] = fmaf(k.w[j][i], dy[i] * act_grad(pre[i], a.act), g[i]);
+  }
+  if (a.d_final && r >= len) {  // a short sequence keeps this row
+    float v[VEC];
+    load_vec<IO, VEC>(static_cast<const IO*>(a.d_final) + (row - len) * a.D + c0, v);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) g[i] += v[i];
+  }
+  store_vec<IO, VEC>(static_cast<IO*>(a.d_past) + row * a.D + c0, g);
+}
+
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
+    conv_bwd_kernel(ConvArgs a, int nvec, int run, int64_t n_blocks,
+                    float* __restrict__ part) {
+  __shared__ float s_part[kBwdRuns][W + 1][kBwdLanes][VEC];
+  const int cv = blockIdx.y * kBwdLanes + threadIdx.x;
+  const bool on = cv < nvec;
+  const int c0 = on ? cv * VEC : 0;
+  Taps<IO, W, VEC> k;
+  k.load(a, c0);
+  if ((int64_t)blockIdx.x >= n_blocks) {  // rows of d_initial_state
+    const int64_t row = ((int64_t)blockIdx.x - n_blocks) * kBwdRuns + threadIdx.y;
+    if (on && row < (int64_t)a.n_seqs * (W - 1)) past_grad<IO, W, VEC>(a, k, row, c0);
+    return;
+  }
+  float dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    db[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+  }
+  const IO* x = static_cast<const IO*>(a.x) + c0;
+  const IO* dy = static_cast<const IO*>(a.d_out) + c0;
+  IO* dx = static_cast<IO*>(a.dx) + c0;
+  int64_t t = ((int64_t)blockIdx.x * kBwdRuns + threadIdx.y) * run;
+  const int64_t t1 = on ? min(t + run, a.tokens) : t;
+  while (t < t1) {
+    SeqCursor q;
+    if (!find_seq(a.cu, a.n_seqs, a.T, (int)t, &q)) break;
+    if (t < q.start) t = q.start;
+    const int64_t e = min((int64_t)q.end, t1);
+    if (t >= e) break;
+    const int64_t stop = min((int64_t)q.end, e + W - 1);
+    float win[W - 1][VEC], g[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      input_at<IO, W, VEC>(a, q, (int)t - (W - 1) + j, c0, win[j]);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
+    }
+    for (int64_t u = t; u < stop; u += kUnroll) {
+      Raw<IO, VEC> rx[kUnroll], ry[kUnroll];
+      const int m = (int)min((int64_t)kUnroll, stop - u);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+        if (i < m) {
+          rx[i] = load_raw<IO, VEC>(x + (u + i) * a.x_stride);
+          ry[i] = load_raw<IO, VEC>(dy + (u + i) * a.D);
+        }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        if (i >= m) break;
+        const int64_t tau = u + i;
+        float xv[VEC], dp[VEC], pre[VEC], done[VEC];
+        unpack(rx[i], xv);
+        unpack(ry[i], dp);
+        taps_dot<IO, W, VEC>(k, win, xv, pre);
+        const bool mine = tau < e;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          dp[c] *= act_grad(pre[c], a.act);
+          if (mine) {
+            db[c] += dp[c];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) dw[j][c] = fmaf(dp[c], win[j][c], dw[j][c]);
+            dw[W - 1][c] = fmaf(dp[c], xv[c], dw[W - 1][c]);
+          }
+          done[c] = fmaf(k.w[0][c], dp[c], g[0][c]);
+#pragma unroll
+          for (int j = 0; j + 1 < W - 1; ++j) g[j][c] = fmaf(k.w[j + 1][c], dp[c], g[j + 1][c]);
+          g[W - 2][c] = k.w[W - 1][c] * dp[c];
+        }
+        const int64_t at = tau - (W - 1);
+        if (at >= t) store_vec<IO, VEC>(dx + at * a.D, done);
+        slide<W, VEC>(win, xv);
+      }
+    }
+    if (stop == q.end) {  // the sequence's last W - 1 places
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        const int64_t at = stop - (W - 1) + j;
+        if (at >= t && at < e) {
+          if (a.d_final) {
+            float v[VEC];
+            load_vec<IO, VEC>(static_cast<const IO*>(a.d_final) +
+                                  ((int64_t)q.s * (W - 1) + j) * a.D + c0, v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g[j][i] += v[i];
+          }
+          store_vec<IO, VEC>(dx + at * a.D, g[j]);
+        }
+      }
+    }
+    t = e;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) s_part[threadIdx.y][j][threadIdx.x][i] = dw[j][i];
+    s_part[threadIdx.y][W][threadIdx.x][i] = db[i];
+  }
+  __syncthreads();
+  // part[block][tap or bias][channel]
+  const int tid = threadIdx.y * kBwdLanes + threadIdx.x;
+  for (int o = tid; o < (W + 1) * kBwdLanes * VEC; o += kBwdLanes * kBwdRuns) {
+    const int j = o / (kBwdLanes * VEC), c = o % (kBwdLanes * VEC);
+    const int ch = blockIdx.y * kBwdLanes * VEC + c;
+    if (ch >= a.D) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int rr = 0; rr < kBwdRuns; ++rr) s += s_part[rr][j][c / VEC][c % VEC];
+    part[((int64_t)blockIdx.x * (W + 1) + j) * a.D + ch] = s;
+  }
+}
+
+// dw[c][j] and db[c]: the blocks' parts summed in a fixed order.
+__global__ void conv_weight_sum_kernel(const float* __restrict__ part, int64_t n_blocks, int W,
+                                       int D, float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float s[8][32];
+  const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
+  float v = 0.f;
+  if (c < D)
+    for (int64_t b = threadIdx.y; b < n_blocks; b += 8) v += part[(b * (W + 1) + j) * D + c];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < D) {
+    for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
+    if (j < W)
+      dw[(int64_t)c * W + j] = v;
+    else if (db)
+      db[c] = v;
+  }
+}
+
+// One thread per (sequence, channel vector): T new tokens, state in place.
+template <typename IO, int W, int VEC>
+__global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a, int nvec) {
+  const int cv = blockIdx.y * blockDim.x + threadIdx.x;
+  const int64_t n = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (cv >= nvec || n >= a.n_seqs) return;
+  const int c0 = cv * VEC;
+  IO* st = static_cast<IO*>(a.final_state) + n * (W - 1) * a.D + c0;
+  Raw<IO, VEC> keep[W - 1], rx;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) keep[j] = load_raw<IO, VEC>(st + (int64_t)j * a.D);
+  const IO* x = static_cast<const IO*>(a.x) + n * a.T * a.x_stride + c0;
+  rx = load_raw<IO, VEC>(x);
+  Taps<IO, W, VEC> k;
+  k.load(a, c0);
+  float win[W - 1][VEC];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) unpack(keep[j], win[j]);
+  IO* out = static_cast<IO*>(a.out) + n * a.T * a.D + c0;
+  for (int t = 0; t < a.T; ++t) {
+    float v[VEC], pre[VEC];
+    unpack(rx, v);
+    if (t + 1 < a.T) rx = load_raw<IO, VEC>(x + (int64_t)(t + 1) * a.x_stride);
+    taps_dot<IO, W, VEC>(k, win, v, pre);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
+    store_vec<IO, VEC>(out + (int64_t)t * a.D, pre);
+    slide<W, VEC>(win, v);
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) store_vec<IO, VEC>(st + (int64_t)j * a.D, win[j]);
+}
+
+// Channel lanes of a 256-thread block: the smallest power of two that covers
+// the channel vectors, so that narrow tensors put several runs in a block.
+dim3 block_shape(int nvec) {
+  int lx = 32;
+  while (lx < 256 && lx < nvec) lx *= 2;
+  return dim3(lx, 256 / lx);
+}
+
+bool vec_ok(const ConvArgs& a, int vec, size_t bytes) {
+  const void* ps[] = {a.x, a.past, a.out, a.final_state, a.d_out, a.d_final, a.dx, a.d_past};
+  for (const void* p : ps)
+    if (p && !aligned_to(p, bytes)) return false;
+  return a.D % vec == 0 && a.x_stride % vec == 0;
+}
+
+template <typename IO, int W, int VEC>
+cudaError_t fwd_launch(const ConvArgs& a, cudaStream_t stream) {
+  const int nvec = a.D / VEC;
+  const dim3 block = block_shape(nvec);
+  // 16 tokens a run re-read 3 of 19 inputs from L2; shorter runs when the
+  // tokens would not give every SM its 2048 threads
+  int run = 16;
+  while (run > 4 && (a.tokens + run - 1) / run * nvec < (int64_t)148 * 2048) run /= 2;
+  const int64_t n_runs = (a.tokens + run - 1) / run;
+  const int64_t rows = n_runs + (a.final_state ? (int64_t)a.n_seqs * (W - 1) : 0);
+  const dim3 grid((unsigned)((rows + block.y - 1) / block.y), (nvec + block.x - 1) / block.x);
+  if (rows) conv_fwd_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec, run, n_runs);
+  return cudaGetLastError();
+}
+
+template <typename IO, int W, int VEC>
+cudaError_t step_launch(const ConvArgs& a, cudaStream_t stream) {
+  const int nvec = a.D / VEC;
+  const dim3 block = block_shape(nvec);
+  const dim3 grid((a.n_seqs + block.y - 1) / block.y, (nvec + block.x - 1) / block.x);
+  conv_step_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec);
+  return cudaGetLastError();
+}
+
+constexpr int kBwdRun = 32;
+int64_t bwd_blocks(const ConvArgs& a) {
+  return (a.tokens + kBwdRun * kBwdRuns - 1) / (kBwdRun * kBwdRuns);
+}
+
+template <typename IO, int W, int VEC>
+cudaError_t bwd_launch(const ConvArgs& a, float* part, cudaStream_t stream) {
+  const int nvec = a.D / VEC;
+  const int64_t blocks = bwd_blocks(a);
+  const int64_t rows = a.d_past ? (int64_t)a.n_seqs * (W - 1) : 0;
+  const dim3 block(kBwdLanes, kBwdRuns);
+  const dim3 grid((unsigned)(blocks + (rows + kBwdRuns - 1) / kBwdRuns),
+                  (nvec + kBwdLanes - 1) / kBwdLanes);
+  if (grid.x)
+    conv_bwd_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec, kBwdRun, blocks, part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  conv_weight_sum_kernel<<<dim3((a.D + 31) / 32, W + 1), dim3(32, 8), 0, stream>>>(
+      part, blocks, W, a.D, a.dw, a.db);
+  return cudaGetLastError();
+}
+
+#define KDA_CONV_W(FN, IO, VEC, ...)                          \
+  (a.W == 2   ? FN<IO, 2, VEC>(__VA_ARGS__)                   \
+   : a.W == 3 ? FN<IO, 3, VEC>(__VA_ARGS__)                   \
+   : a.W == 4 ? FN<IO, 4, VEC>(__VA_ARGS__)                   \
+              : cudaErrorInvalidValue)
+
+}  // namespace
+
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream) {
+  if (a.bf16)
+    return vec_ok(a, 8, 16) ? KDA_CONV_W(fwd_launch, __nv_bfloat16, 8, a, stream)
+                            : KDA_CONV_W(fwd_launch, __nv_bfloat16, 1, a, stream);
+  return vec_ok(a, 4, 16) ? KDA_CONV_W(fwd_launch, float, 4, a, stream)
+                          : KDA_CONV_W(fwd_launch, float, 1, a, stream);
+}
+
+cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t stream) {
+  if (a.n_seqs == 0 || a.T == 0) return cudaSuccess;
+  if (a.bf16)
+    return vec_ok(a, 8, 16) ? KDA_CONV_W(step_launch, __nv_bfloat16, 8, a, stream)
+                            : KDA_CONV_W(step_launch, __nv_bfloat16, 1, a, stream);
+  return vec_ok(a, 4, 16) ? KDA_CONV_W(step_launch, float, 4, a, stream)
+                          : KDA_CONV_W(step_launch, float, 1, a, stream);
+}
+
+size_t conv_bwd_workspace_bytes(const ConvArgs& a) {
+  return (size_t)bwd_blocks(a) * (a.W + 1) * a.D * sizeof(float);
+}
+
+cudaError_t launch_conv_bwd(const ConvArgs& a, void* ws, cudaStream_t stream) {
+  float* part = static_cast<float*>(ws);
+  if (a.bf16)
+    return vec_ok(a, 4, 8) ? KDA_CONV_W(bwd_launch, __nv_bfloat16, 4, a, part, stream)
+                           : KDA_CONV_W(bwd_launch, __nv_bfloat16, 1, a, part, stream);
+  return vec_ok(a, 4, 16) ? KDA_CONV_W(bwd_launch, float, 4, a, part, stream)
+                          : KDA_CONV_W(bwd_launch, float, 1, a, part, stream);
+}
+
+}  // namespace kda

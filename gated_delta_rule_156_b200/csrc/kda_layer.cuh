@@ -1,0 +1,132 @@
+// Shared by the layer operators (short convolution, selective scan, block
+// norm): launch arguments, vector loads, activations, sequence lookup.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_common.cuh"
+#include "kda_layer_internal.h"
+
+namespace kda {
+
+// VEC consecutive elements as fp32, in one access of VEC * sizeof(IO) bytes
+// (the address must be aligned to that).
+template <typename IO, int VEC>
+struct Raw;  // storage of VEC elements
+template <>
+struct Raw<__nv_bfloat16, 1> { uint16_t r; };
+template <>
+struct Raw<__nv_bfloat16, 4> { uint2 r; };
+template <>
+struct Raw<__nv_bfloat16, 8> { uint4 r; };
+template <>
+struct Raw<float, 1> { float r; };
+template <>
+struct Raw<float, 4> { float4 r; };
+template <>
+struct Raw<float, 8> { float4 r[2]; };
+
+template <typename IO, int VEC>
+__device__ __forceinline__ Raw<IO, VEC> load_raw(const IO* p) {
+  return *reinterpret_cast<const Raw<IO, VEC>*>(p);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 1>& a, float (&v)[1]) {
+  v[0] = __uint_as_float((uint32_t)a.r << 16);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 4>& a, float (&v)[4]) {
+  v[0] = bf_lo(a.r.x); v[1] = bf_hi(a.r.x); v[2] = bf_lo(a.r.y); v[3] = bf_hi(a.r.y);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& a, float (&v)[8]) {
+  v[0] = bf_lo(a.r.x); v[1] = bf_hi(a.r.x); v[2] = bf_lo(a.r.y); v[3] = bf_hi(a.r.y);
+  v[4] = bf_lo(a.r.z); v[5] = bf_hi(a.r.z); v[6] = bf_lo(a.r.w); v[7] = bf_hi(a.r.w);
+}
+__device__ __forceinline__ void unpack(const Raw<float, 1>& a, float (&v)[1]) { v[0] = a.r; }
+__device__ __forceinline__ void unpack(const Raw<float, 4>& a, float (&v)[4]) {
+  v[0] = a.r.x; v[1] = a.r.y; v[2] = a.r.z; v[3] = a.r.w;
+}
+__device__ __forceinline__ void unpack(const Raw<float, 8>& a, float (&v)[8]) {
+  v[0] = a.r[0].x; v[1] = a.r[0].y; v[2] = a.r[0].z; v[3] = a.r[0].w;
+  v[4] = a.r[1].x; v[5] = a.r[1].y; v[6] = a.r[1].z; v[7] = a.r[1].w;
+}
+
+__device__ __forceinline__ uint32_t bf_pair(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ void pack(const float (&v)[1], Raw<__nv_bfloat16, 1>& a) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v[0]);
+  a.r = *reinterpret_cast<const uint16_t*>(&b);
+}
+__device__ __forceinline__ void pack(const float (&v)[4], Raw<__nv_bfloat16, 4>& a) {
+  a.r = make_uint2(bf_pair(v[0], v[1]), bf_pair(v[2], v[3]));
+}
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<__nv_bfloat16, 8>& a) {
+  a.r = make_uint4(bf_pair(v[0], v[1]), bf_pair(v[2], v[3]), bf_pair(v[4], v[5]),
+                   bf_pair(v[6], v[7]));
+}
+__device__ __forceinline__ void pack(const float (&v)[1], Raw<float, 1>& a) { a.r = v[0]; }
+__device__ __forceinline__ void pack(const float (&v)[4], Raw<float, 4>& a) {
+  a.r = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<float, 8>& a) {
+  a.r[0] = make_float4(v[0], v[1], v[2], v[3]);
+  a.r[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+template <typename IO, int VEC>
+__device__ __forceinline__ void load_vec(const IO* p, float (&v)[VEC]) {
+  unpack(load_raw<IO, VEC>(p), v);
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void store_vec(IO* p, const float (&v)[VEC]) {
+  Raw<IO, VEC> a;
+  pack(v, a);
+  *reinterpret_cast<Raw<IO, VEC>*>(p) = a;
+}
+
+__device__ __forceinline__ float sigmoid_f(float x) {
+  return __fdividef(1.f, 1.f + __expf(-x));
+}
+// d silu(x) / dx from x and s = sigmoid(x)
+__device__ __forceinline__ float silu_grad(float x, float s) {
+  return s * fmaf(x, 1.f - s, 1.f);
+}
+// log(1 + exp(x)); log1pf keeps the small steps of very negative x exact
+__device__ __forceinline__ float softplus_f(float x) {
+  return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x)));
+}
+
+// The sequence that owns a token of the flat token axis.
+struct SeqCursor {
+  int s, start, end;  // token range [start, end) of sequence s
+};
+// First sequence whose end lies behind token t (its start may lie behind t as
+// well: a gap).  Returns false when there is none.
+__device__ __forceinline__ bool find_seq(const int32_t* cu, int n_seqs, int T,
+                                         int t, SeqCursor* c) {
+  if (cu == nullptr) {
+    c->s = t / T;
+    c->start = c->s * T;
+    c->end = c->start + T;
+    return c->s < n_seqs;
+  }
+  int lo = 0, hi = n_seqs;  // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (clampi(cu[mid + 1], 0, T) > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  if (lo >= n_seqs) return false;
+  c->s = lo;
+  seq_range(cu, lo, T, &c->start, &c->end);
+  return c->end > t;
+}
+
+}  // namespace kda

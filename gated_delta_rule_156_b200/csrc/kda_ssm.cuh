@@ -1,0 +1,104 @@
+// Shared by the selective scan's forward and backward: the split of channels
+// and states over lanes, the staged tile of one token range, and sums over
+// lanes.
+//
+//   step_t = softplus(delta_t + bias);  a_t[n] = exp(step_t A[n])
+//   h_t[n] = a_t[n] h_{t-1}[n] + step_t u_t B_t[n];  y_t = sum_n C_t[n] h_t[n]
+//
+// A lane owns 4 states of one channel; L lanes hold a channel's states
+// (4 L >= S, absent states have A = B = C = 0 and stay 0), a CTA of 128
+// threads holds 128 / L channels of one group and one sequence and walks the
+// sequence in tiles of tokens.  Per (token, channel) a tile keeps step and
+// step * u, per token the 4 L values of B and of C, all fp32 in shared memory.
+#pragma once
+
+#include "kda_layer.cuh"
+
+namespace kda {
+
+constexpr int kSsmThreads = 128;
+constexpr int kSsmStates = 4;  // states per lane
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The channels of a CTA: channel blocks are counted group by group.
+struct SsmBlock {
+  int g, c0, n;  // group, first channel, channels (<= CH)
+  __device__ __forceinline__ SsmBlock(const SsmArgs& a, int ch, int block) {
+    const int per = a.D / a.G, nb = (per + ch - 1) / ch;
+    g = block / nb;
+    const int k = block % nb;
+    c0 = g * per + k * ch;
+    n = min(ch, per - k * ch);
+  }
+};
+
+// Sum of NV values over the lanes that differ in the bits of `mask`, spread:
+// while there are values to halve, each exchange keeps one half of them; the
+// rest are plain exchanges.  Returns with v[0 .. NV/lanes) (at least one)
+// holding the totals of values first .. first + that many.
+template <int NV, int LOW, int HIGH>
+struct SpreadSum {  // lanes LOW, 2 LOW, ... < HIGH
+  static __device__ __forceinline__ void run(float (&v)[NV], int lane, int& first) {
+    if constexpr (LOW < HIGH) {
+      if constexpr (NV > 1) {
+        constexpr int HALF = NV / 2;
+        const bool up = lane & LOW;
+        float w[HALF];
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) {
+          const float keep = up ? v[i + HALF] : v[i];
+          const float give = up ? v[i] : v[i + HALF];
+          w[i] = keep + __shfl_xor_sync(0xffffffffu, give, LOW);
+        }
+        if (up) first += HALF;
+        SpreadSum<HALF, LOW * 2, HIGH>::run(w, lane, first);
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) v[i] = w[i];
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], LOW);
+        SpreadSum<1, LOW * 2, HIGH>::run(v, lane, first);
+      }
+    }
+  }
+};
+
+// Chunk ids of the backward's saved states: chunk c (of 8 tokens) of sequence
+// s has id start_s / 8 + s + c.  The ids of two sequences never meet, since
+// floor((start + len) / 8) + 1 >= floor(start / 8) + ceil(len / 8), and are
+// below tokens / 8 + n_seqs + 1.
+constexpr int kSsmChunk = 8;
+__host__ __device__ __forceinline__ int64_t ssm_chunk_id(int s, int start, int c) {
+  return (int64_t)(start / kSsmChunk) + s + c;
+}
+
+// What the forward kernel does with a token's result.
+enum SsmMode {
+  kSsmOut,   // out = y silu(z)
+  kSsmSave,  // backward's first pass: saved states, and dz = d_out y silu'(z)
+};
+struct SsmSave {
+  float* states;      // [chunk ids][D][S]
+  const void* d_out;  // for dz
+  void* dz;           // or null
+};
+cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, cudaStream_t stream);
+
+// Lanes per channel for S states: the smallest power of two >= S / 4, at
+// least 2 (so that a CTA never holds more than 64 channels).
+inline int ssm_lanes(int S) {
+  int l = 2;
+  while (l * kSsmStates < S) l *= 2;
+  return l;
+}
+__host__ __device__ inline int ssm_blocks(const SsmArgs& a, int ch) {
+  const int per = a.D / a.G;
+  return a.G * ((per + ch - 1) / ch);
+}
+
+}  // namespace kda

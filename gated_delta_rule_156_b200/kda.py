@@ -18,7 +18,8 @@ STATUS_NAMES = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED",
                 3: "KDA_ERR_MISALIGNED", 4: "KDA_ERR_CUDA", 5: "KDA_ERR_TIMEOUT",
                 6: "KDA_ERR_RANGE"}
 
-# Entry points declared in include/kda.h (kept in sync by tests).
+# Entry points declared in include/kda.h and include/kda_layer.h (kept in sync
+# by tests).
 EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_staged", "kda_recurrent_step",
            "kda_chunk_fwd_plan", "kda_selftest_umma", "kda_device_status",
            "kda_status_string", "kda_last_cuda_error", "kda_version",
@@ -28,8 +29,12 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_staged", "kda_recurrent_step",
            "kda_chunk_bwd_plan", "kda_chunk_fwd_split", "kda_workspace_pool",
            "kda_chunk_fwd_twopass", "kda_chunk_fwd_paired",
            "kda_chunk_fwd_split_plan", "kda_profile_pass_event",
-           "kda_chunk_bwd_layout")
+           "kda_chunk_bwd_layout", "kda_short_conv_fwd", "kda_short_conv_bwd",
+           "kda_short_conv_step", "kda_ssm_scan_fwd", "kda_ssm_scan_bwd",
+           "kda_ssm_scan_bwd_plan", "kda_ssm_step", "kda_block_norm_fwd",
+           "kda_block_norm_bwd")
 GATES = {"channel": 0, "head": 1, "none": 2}
+ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
 
 
 class KdaShape(ctypes.Structure):
@@ -42,6 +47,33 @@ class KdaShape(ctypes.Structure):
 class KdaPrologue(ctypes.Structure):
     _fields_ = [("normalize_qk", ctypes.c_int), ("q_scale", ctypes.c_float),
                 ("gate_logits", ctypes.c_int), ("gate_scale", ctypes.c_float)]
+
+
+class KdaConvShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("W", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("io_dtype", ctypes.c_int), ("activation", ctypes.c_int),
+                ("x_stride", ctypes.c_int64)]
+
+
+class KdaSsmShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("S", ctypes.c_int), ("G", ctypes.c_int),
+                ("n_seqs", ctypes.c_int), ("io_dtype", ctypes.c_int),
+                ("softplus", ctypes.c_int), ("u_stride", ctypes.c_int64),
+                ("delta_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64),
+                ("b_group_stride", ctypes.c_int64),
+                ("c_stride", ctypes.c_int64),
+                ("c_group_stride", ctypes.c_int64)]
+
+
+class KdaNormShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int),
+                ("width", ctypes.c_int), ("io_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("gate_act", ctypes.c_int),
+                ("gate_first", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
 
 
 def _prologue(pro):
@@ -148,6 +180,22 @@ def library():
         lib.kda_device_status.argtypes = [vp]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
+        for name, struct, n in (("kda_short_conv_fwd", KdaConvShape, 7),
+                                ("kda_short_conv_bwd", KdaConvShape, 11),
+                                ("kda_short_conv_step", KdaConvShape, 5),
+                                ("kda_ssm_scan_fwd", KdaSsmShape, 12),
+                                ("kda_ssm_scan_bwd", KdaSsmShape, 21),
+                                ("kda_ssm_step", KdaSsmShape, 10),
+                                ("kda_block_norm_fwd", KdaNormShape, 8),
+                                ("kda_block_norm_bwd", KdaNormShape, 14)):
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            # the shape, n tensors, the stream
+            fn.argtypes = [ctypes.POINTER(struct)] + [vp] * (n + 1)
+        lib.kda_ssm_scan_bwd_plan.restype = ctypes.c_int
+        lib.kda_ssm_scan_bwd_plan.argtypes = [
+            ctypes.POINTER(KdaSsmShape), ctypes.c_int,
+            ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_workspace_pool.restype = ctypes.c_int
         lib.kda_workspace_pool.argtypes = [ctypes.POINTER(ctypes.c_size_t),
                                            ctypes.POINTER(ctypes.c_size_t)]
@@ -530,3 +578,438 @@ def selftest_timeout(limit_us=1000, stream=None):
     st = library().kda_selftest_timeout(int(limit_us), _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_selftest_timeout")
+
+
+# ---- the operators around a recurrent layer (include/kda_layer.h) ----------
+
+class _On:
+    """The device of a call's tensors and the stream it is queued on.  The
+    call runs with that device current, and what it allocates belongs to that
+    stream, so it may be made from any device or stream; the caller orders
+    the stream behind whatever wrote the inputs."""
+
+    def __init__(self, t, stream):
+        self.dev, self.stream = t.device, stream
+
+    def __enter__(self):
+        self.old_dev = self.old_stream = None
+        if self.dev.index != torch.cuda.current_device():
+            self.old_dev = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        cur = torch.cuda.current_stream(self.dev)
+        if self.stream is not None and self.stream != cur:
+            if self.stream.device != self.dev:
+                self._leave()
+                raise ValueError("the stream must be on the tensors' device")
+            self.old_stream = cur
+            torch.cuda.set_stream(self.stream)
+            cur = self.stream
+        return cur.cuda_stream
+
+    def _leave(self):
+        if self.old_stream is not None:
+            torch.cuda.set_stream(self.old_stream)
+        if self.old_dev is not None:
+            torch.cuda.set_device(self.old_dev)
+
+    def __exit__(self, *exc):
+        self._leave()
+
+
+def _need(name, t, dev, dtype, shape, optional=False):
+    """A dense tensor of this dtype and shape on dev (None where optional)."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor) or t.device != dev or \
+            dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on one device with "
+                         "the others")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _tokens(name, t, dev, dtype, shape, inner=1):
+    """A tensor of this shape whose leading dims are tokens and whose last
+    `inner` dims are one token's elements: dense within a token, tokens at one
+    stride (a slice of a wider tensor will do).  Returns the stride."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or \
+            dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on one device with "
+                         "the others")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    if t.is_contiguous() or t.numel() == 0:
+        return 0
+    stride = _token_stride(t, inner)
+    if stride is None:
+        raise ValueError(f"{name}: a token's elements must be dense and "
+                         "consecutive tokens one stride apart")
+    return stride
+
+
+def _token_stride(t, inner):
+    """The stride between the tokens of t (0: there is one token at most),
+    None where its elements do not lie that way."""
+    shape, st, lead = t.shape, t.stride(), t.dim() - inner
+    width = 1
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != width:
+            return None
+        width *= shape[i]
+    stride = None  # dims of size 1 have no stride
+    for i in range(lead - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if stride is None:
+            stride = st[i]
+            if stride < width:
+                return None
+            span = stride * shape[i]
+        elif st[i] == span:
+            span *= shape[i]
+        else:
+            return None
+    return stride or 0
+
+
+def _groups(name, t, dev, dtype, shape):
+    """(token stride, group stride) of B or C [B, T, G, S]."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or \
+            dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on one device with "
+                         "the others")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous() or t.numel() == 0:
+        return 0, 0
+    b, n, g, s = shape
+    st = t.stride()
+    if s > 1 and st[3] != 1:
+        raise ValueError(f"{name}: a group's states must be dense")
+    group = st[2] if g > 1 else s
+    if b > 1 and n > 1 and st[0] != n * st[1]:
+        raise ValueError(f"{name}: consecutive tokens must be one stride "
+                         "apart")
+    token = st[1] if n > 1 else st[0] if b > 1 else g * group
+    if group < s or token < (g - 1) * group + s:
+        raise ValueError(f"{name}: tokens and groups must not overlap")
+    return token, group
+
+
+def _batch(x, cu_seqlens, name):
+    """(B, T, sequences) of a [B, T, ...] tensor, dense or packed."""
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or \
+            x.dim() < 3:
+        raise ValueError(f"{name} must be a CUDA tensor [B, T, ...]")
+    B, T = x.shape[:2]
+    if cu_seqlens is None:
+        return B, T, B
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
+    if B != 1:
+        raise ValueError("a packed batch has B == 1")
+    n = cu_seqlens.numel() - 1
+    _need("cu_seqlens", cu_seqlens, x.device, torch.int32, (n + 1,))
+    return B, T, n
+
+
+def _run(name, shape, tensors, stream):
+    fn = getattr(library(), name)
+    st = fn(ctypes.byref(shape),
+            *[None if t is None else t.data_ptr() for t in tensors], stream)
+    if st != KDA_OK:
+        raise KdaError(st, name)
+
+
+def _conv_shape(x, weight, bias, cu_seqlens, activation):
+    B, T, n = _batch(x, cu_seqlens, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, D]")
+    D, dev, f32 = x.shape[2], x.device, torch.float32
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [D, W]")
+    W = weight.shape[1]
+    _need("weight", weight, dev, f32, (D, W))
+    _need("bias", bias, dev, f32, (D,), optional=True)
+    stride = _tokens("x", x, dev, x.dtype, x.shape)
+    shape = KdaConvShape(B, T, D, W, n if cu_seqlens is not None else 0,
+                         _io(x), ACTS[activation], stride)
+    return shape, (B, T, D), (n, W - 1, D)
+
+
+def short_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None,
+                   activation="silu", want_final_state=True, out=None,
+                   stream=None):
+    """Depthwise causal convolution over each sequence (kda_short_conv_fwd).
+
+    x [B, T, D] (bf16 or fp32; may be a slice of a projection's output),
+    weight [D, W] fp32 with W in {2, 3, 4}, bias [D] fp32 or None,
+    initial_state [N, W-1, D] like x or None (zeros), activation "silu" or
+    "none".  Returns (out [B, T, D], final_state [N, W-1, D] or None).
+    """
+    shape, full, state = _conv_shape(x, weight, bias, cu_seqlens, activation)
+    dev, dt = x.device, x.dtype
+    _need("initial_state", initial_state, dev, dt, state, optional=True)
+    _need("out", out, dev, dt, full, optional=True)
+    with _On(x, stream) as s:
+        if out is None:
+            out = torch.empty(full, dtype=dt, device=dev)
+        final = torch.empty(state, dtype=dt, device=dev) \
+            if want_final_state else None
+        _run("kda_short_conv_fwd", shape,
+             (x, weight, bias, initial_state, cu_seqlens, out, final), s)
+    return out, final
+
+
+def short_conv_bwd(x, weight, bias, initial_state, cu_seqlens, d_out,
+                   d_final_state=None, activation="silu",
+                   want_initial_state=True, stream=None):
+    """Gradients of short_conv_fwd (kda_short_conv_bwd): (dx, d_weight,
+    d_bias or None, d_initial_state or None)."""
+    shape, full, state = _conv_shape(x, weight, bias, cu_seqlens, activation)
+    dev, dt = x.device, x.dtype
+    _need("initial_state", initial_state, dev, dt, state, optional=True)
+    _need("d_out", d_out, dev, dt, full)
+    _need("d_final_state", d_final_state, dev, dt, state, optional=True)
+    with _On(x, stream) as s:
+        dx = torch.empty(full, dtype=dt, device=dev)
+        dw = torch.empty_like(weight)
+        db = None if bias is None else torch.empty_like(bias)
+        d0 = torch.empty(state, dtype=dt, device=dev) \
+            if want_initial_state else None
+        _run("kda_short_conv_bwd", shape,
+             (x, weight, bias, initial_state, cu_seqlens, d_out,
+              d_final_state, dx, dw, db, d0), s)
+    return dx, dw, db, d0
+
+
+def short_conv_step(x, weight, bias, state, activation="silu", out=None,
+                    stream=None):
+    """The convolution of T >= 1 new tokens (kda_short_conv_step): x
+    [N, T, D]; ``state`` [N, W-1, D] is updated in place.  Returns out."""
+    shape, full, st = _conv_shape(x, weight, bias, None, activation)
+    dev, dt = x.device, x.dtype
+    _need("state", state, dev, dt, st)
+    _need("out", out, dev, dt, full, optional=True)
+    with _On(x, stream) as s:
+        if out is None:
+            out = torch.empty(full, dtype=dt, device=dev)
+        _run("kda_short_conv_step", shape, (x, weight, bias, state, out), s)
+    return out
+
+
+def _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias, cu_seqlens, softplus):
+    B, T, n = _batch(u, cu_seqlens, "u")
+    if u.dim() != 3 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
+            not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
+        raise ValueError("u must be [B, T, D], A [D, S], Bm [B, T, G, S]")
+    C, S, G = u.shape[2], A.shape[1], Bm.shape[2]
+    dev, dt, f32 = u.device, u.dtype, torch.float32
+    _need("A", A, dev, f32, (C, S))
+    _need("D", D, dev, f32, (C,), optional=True)
+    _need("delta_bias", delta_bias, dev, f32, (C,), optional=True)
+    us = _tokens("u", u, dev, dt, u.shape)
+    ds = _tokens("delta", delta, dev, dt, u.shape)
+    zs = 0 if z is None else _tokens("z", z, dev, dt, u.shape)
+    bs, bg = _groups("Bm", Bm, dev, dt, (B, T, G, S))
+    cs, cg = _groups("Cm", Cm, dev, dt, (B, T, G, S))
+    shape = KdaSsmShape(B, T, C, S, G, n if cu_seqlens is not None else 0,
+                        _io(u), int(bool(softplus)), us, ds, zs, bs, bg, cs,
+                        cg)
+    return shape, (n, C, S)
+
+
+def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
+                 initial_state=None, cu_seqlens=None, softplus=True, out=None,
+                 final_state=None, stream=None):
+    """Selective state space scan (kda_ssm_scan_fwd).
+
+    u, delta, z [B, T, D] and Bm, Cm [B, T, G, S] (bf16 or fp32, one dtype;
+    slices of a projection's output will do; z may be None), A [D, S], D and
+    delta_bias [D] fp32 (may be None), initial_state [N, D, S] fp32 or None.
+    Returns (out [B, T, D], final_state [N, D, S] fp32); ``final_state`` may
+    be the initial state itself.
+    """
+    shape, state = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias,
+                              cu_seqlens, softplus)
+    dev, dt, f32 = u.device, u.dtype, torch.float32
+    _need("initial_state", initial_state, dev, f32, state, optional=True)
+    _need("out", out, dev, dt, u.shape, optional=True)
+    _need("final_state", final_state, dev, f32, state, optional=True)
+    with _On(u, stream) as s:
+        if out is None:
+            out = torch.empty(u.shape, dtype=dt, device=dev)
+        if final_state is None:
+            final_state = torch.empty(state, dtype=f32, device=dev)
+        _run("kda_ssm_scan_fwd", shape,
+             (u, delta, A, Bm, Cm, D, z, delta_bias, initial_state,
+              cu_seqlens, out, final_state), s)
+    return out, final_state
+
+
+def ssm_scan_bwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
+                 initial_state=None, cu_seqlens=None, d_out=None,
+                 d_final_state=None, softplus=True, want_initial_state=True,
+                 stream=None):
+    """Gradients of ssm_scan_fwd (kda_ssm_scan_bwd): (du, d_delta, dA, dBm,
+    dCm, dD, dz, d_delta_bias, d_initial_state), None where the input is
+    None (d_initial_state: unless want_initial_state)."""
+    shape, state = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias,
+                              cu_seqlens, softplus)
+    dev, dt, f32 = u.device, u.dtype, torch.float32
+    _need("initial_state", initial_state, dev, f32, state, optional=True)
+    _need("d_out", d_out, dev, dt, u.shape)
+    _need("d_final_state", d_final_state, dev, f32, state, optional=True)
+    with _On(u, stream) as s:
+        du = torch.empty(u.shape, dtype=dt, device=dev)
+        dd = torch.empty(u.shape, dtype=dt, device=dev)
+        dA = torch.empty_like(A)
+        dB = torch.empty(Bm.shape, dtype=dt, device=dev)
+        dC = torch.empty(Bm.shape, dtype=dt, device=dev)
+        dD = None if D is None else torch.empty_like(D)
+        dz = None if z is None else torch.empty(u.shape, dtype=dt, device=dev)
+        db = None if delta_bias is None else torch.empty_like(delta_bias)
+        d0 = torch.empty(state, dtype=f32, device=dev) \
+            if want_initial_state else None
+        _run("kda_ssm_scan_bwd", shape,
+             (u, delta, A, Bm, Cm, D, z, delta_bias, initial_state,
+              cu_seqlens, d_out, d_final_state, du, dd, dA, dB, dC, dD, dz,
+              db, d0), s)
+    return du, dd, dA, dB, dC, dD, dz, db, d0
+
+
+def ssm_scan_bwd_plan(B, T, D, S, G, dtype, packed=False, n_seqs=0):
+    """(kernels, workspace_bytes) of an ssm_scan_bwd call of this shape."""
+    io = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    shape = KdaSsmShape(B, T, D, S, G, n_seqs if packed else 0, io, 1)
+    kern, ws = ctypes.c_int(), ctypes.c_size_t()
+    st = library().kda_ssm_scan_bwd_plan(ctypes.byref(shape), int(packed),
+                                         ctypes.byref(kern), ctypes.byref(ws))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_ssm_scan_bwd_plan")
+    return kern.value, ws.value
+
+
+def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None,
+             softplus=True, out=None, stream=None):
+    """The scan over T >= 1 new tokens (kda_ssm_step): u, delta, z [N, T, D],
+    Bm, Cm [N, T, G, S]; ``state`` [N, D, S] fp32 is updated in place.
+    Returns out [N, T, D]."""
+    shape, st = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias, None,
+                           softplus)
+    dev, dt = u.device, u.dtype
+    _need("state", state, dev, torch.float32, st)
+    _need("out", out, dev, dt, u.shape, optional=True)
+    with _On(u, stream) as s:
+        if out is None:
+            out = torch.empty(u.shape, dtype=dt, device=dev)
+        _run("kda_ssm_step", shape,
+             (u, delta, A, Bm, Cm, D, z, delta_bias, state, out), s)
+    return out
+
+
+def _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
+                gate_act, gate_first, eps):
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or \
+            x.dim() < 2:
+        raise ValueError("x must be a CUDA tensor [..., width]")
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    width = x.shape[-1]
+    if width == 0:
+        raise ValueError("x must have a width")
+    # rows at one stride, else tokens of `heads` dense rows at one stride
+    inner = 1
+    for t in (x, gate):
+        if isinstance(t, torch.Tensor) and not t.is_contiguous() and \
+                t.dim() > 2 and _token_stride(t, 1) is None:
+            inner = 2
+    heads = x.shape[-2] if inner == 2 else 1
+    tokens = x.numel() // (heads * width) if x.numel() else 0
+    _need("post_weight", post_weight, dev, f32, (width,), optional=True)
+    _need("scale", scale, dev, f32, (width,), optional=True)
+    _need("pre_weight", pre_weight, dev, f32, (width,), optional=True)
+    _need("residual", residual, dev, rt, x.shape, optional=True)
+    xs = _tokens("x", x, dev, dt, x.shape, inner)
+    gs = 0 if gate is None else _tokens("gate", gate, dev, dt, x.shape, inner)
+    if rt not in (dt, f32):
+        raise ValueError(f"the residual must be {dt} or float32, got {rt}")
+    return KdaNormShape(tokens, max(heads, 1), width, _io(x),
+                        KDA_BF16 if rt == torch.bfloat16 else KDA_F32,
+                        ACTS[gate_act], int(bool(gate_first)), float(eps), xs,
+                        gs)
+
+
+def block_norm_fwd(x, post_weight=None, gate=None, residual=None, scale=None,
+                   pre_weight=None, gate_act="sigmoid", gate_first=False,
+                   eps=1e-6, out=None, normed=None, stream=None):
+    """The norm after a block with its gate, the residual scale and sum, and
+    the next block's norm (kda_block_norm_fwd), each part optional:
+
+        h = x [act(gate) with gate_first]
+        p = rms(h) post_weight [act(gate) otherwise]
+        out = residual + scale p;  normed = rms(out) pre_weight
+
+    x, gate [..., width] (bf16 or fp32; the norms are over the last dim;
+    slices of a projection's output will do, [..., heads, width] with dense
+    tokens or rows at one stride), residual the
+    same shape in x's dtype or fp32, weights and scale [width] fp32,
+    ``gate_act`` "sigmoid", "silu" or "none".  ``out`` may be the residual
+    itself.  Returns (out in the residual's dtype, normed in x's or None).
+    """
+    rt = residual.dtype if isinstance(residual, torch.Tensor) else \
+        out.dtype if isinstance(out, torch.Tensor) else x.dtype
+    shape = _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
+                        gate_act, gate_first, eps)
+    dev, dt = x.device, x.dtype
+    _need("out", out, dev, rt, x.shape, optional=True)
+    _need("normed", normed, dev, dt, x.shape, optional=True)
+    with _On(x, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=rt, device=dev)
+        if normed is None and pre_weight is not None:
+            normed = torch.empty(x.shape, dtype=dt, device=dev)
+        _run("kda_block_norm_fwd", shape,
+             (x, post_weight, gate, residual, scale, pre_weight, out, normed),
+             s)
+    return out, normed
+
+
+def block_norm_bwd(x, post_weight=None, gate=None, residual=None, scale=None,
+                   pre_weight=None, d_out=None, d_normed=None,
+                   gate_act="sigmoid", gate_first=False, eps=1e-6,
+                   stream=None):
+    """Gradients of block_norm_fwd (kda_block_norm_bwd): (dx, dgate,
+    d_residual, d_post_weight, d_scale, d_pre_weight), None where the input
+    is None.  d_out has the dtype of out, d_normed of x; either may be None
+    (zero)."""
+    rt = residual.dtype if isinstance(residual, torch.Tensor) else \
+        d_out.dtype if isinstance(d_out, torch.Tensor) else x.dtype
+    shape = _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
+                        gate_act, gate_first, eps)
+    dev, dt = x.device, x.dtype
+    _need("d_out", d_out, dev, rt, x.shape, optional=True)
+    _need("d_normed", d_normed, dev, dt, x.shape, optional=True)
+
+    def like(t, dtype):
+        return None if t is None else torch.empty(t.shape, dtype=dtype,
+                                                  device=dev)
+    with _On(x, stream) as s:
+        dx, dg, dr = like(x, dt), like(gate, dt), like(residual, rt)
+        f32 = torch.float32
+        dpost, dscale, dpre = (like(t, f32) for t in
+                               (post_weight, scale, pre_weight))
+        _run("kda_block_norm_bwd", shape,
+             (x, post_weight, gate, residual, scale, pre_weight, d_out,
+              d_normed, dx, dg, dr, dpost, dscale, dpre), s)
+    return dx, dg, dr, dpost, dscale, dpre
