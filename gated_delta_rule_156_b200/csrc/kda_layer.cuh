@@ -96,9 +96,43 @@ __device__ __forceinline__ float sigmoid_f(float x) {
 __device__ __forceinline__ float silu_grad(float x, float s) {
   return s * fmaf(x, 1.f - s, 1.f);
 }
-// log(1 + exp(x)); log1pf keeps the small steps of very negative x exact
+// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|).  With s = e / (2 + e),
+// log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...): s <= 1/3, so seven
+// terms leave 2e-8 of the value, for the smallest steps too (a logarithm of
+// 1 + e would lose them).
 __device__ __forceinline__ float softplus_f(float x) {
-  return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x)));
+  const float e = __expf(-fabsf(x));
+  const float s = __fdividef(e, 2.f + e), q = s * s;
+  float p = 1.f / 13.f;
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return fmaf(2.f * s, p, fmaxf(x, 0.f));
+}
+
+// Two fp32 values in one 64-bit register pair, and the packed arithmetic on
+// them (one instruction for two results, same rounding as two).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // The sequence that owns a token of the flat token axis.

@@ -12,115 +12,306 @@ namespace kda {
 
 namespace {
 
-constexpr int kTile = 32;  // tokens per tile
+constexpr int kHelpers = 128;  // helper threads
 
-template <typename IO, int L, int MODE>
-__global__ void __launch_bounds__(kSsmThreads) ssm_fwd_kernel(SsmArgs a, SsmSave save) {
-  constexpr int CH = kSsmThreads / L, SW = L * kSsmStates;
-  __shared__ float2 s_dt[kTile][CH];
-  __shared__ float s_y[kTile][CH];
-  __shared__ __align__(16) float s_b[kTile][SW], s_c[kTile][SW];
-  const int tid = threadIdx.x, l = tid % L, ch = tid / L;
+// Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
+// (a helper then holds 8 pairs as with four lanes, and nothing spills).
+constexpr int tile_of(int lanes) { return lanes == 2 ? 16 : 32; }
+
+// A CTA's shared memory, two of each: the tile in work and the next.
+template <int L, bool WANT_Y>
+struct FwdShared {
+  static constexpr int TILE = tile_of(L), CH = kSsmThreads / L, SW = L * kSsmStates;
+  static constexpr int YP = CH + 8;  // row pitch of y: 4 tokens of 8 channels on 32 banks
+  float2 dt[2][TILE][CH];            // step, step * u
+  float b[2][TILE][SW];
+  float c[2][WANT_Y ? TILE : 1][SW];
+  float y[2][WANT_Y ? TILE : 1][YP];
+};
+
+// N consecutive elements in one access where VEC, else one by one.
+template <typename IO, int N>
+struct __align__(N * sizeof(IO) >= 16 ? 16 : N * sizeof(IO)) Elems {
+  IO v[N];
+};
+
+// CTA: 4 warps run the recurrence, 4 helper warps feed them and finish their
+// results, tile by tile of 32 tokens with one barrier a tile: while the
+// recurrence runs tile i, the helpers turn tile i + 1 into step, step * u, B
+// and C (its loads were issued a tile earlier and wait in registers), finish
+// and store tile i - 1, and issue the loads of tile i + 2.  A helper thread
+// keeps what a token's result needs besides y (skip * u, silu(z)) in
+// registers, since it stores the same elements it loaded.
+template <typename IO, int L, int MODE, bool VEC>
+__global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
+    ssm_fwd_kernel(SsmArgs a, SsmSave save, SsmSplit split) {
+  constexpr bool WANT_Y = MODE == kSsmOut || MODE == kSsmSaveDz;
+  using Shared = FwdShared<L, WANT_Y>;
+  constexpr int CH = Shared::CH, SW = Shared::SW, kTile = Shared::TILE;
+  constexpr int E = kTile * CH / kHelpers;   // (token, channel) pairs a helper
+  constexpr int BN = kTile * SW / kHelpers;  // values of B (and of C) a helper
+  constexpr int TPT = kHelpers / kTile;      // helpers a token
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(s_raw);
+  auto& s_dt = sh.dt;
+  auto& s_b = sh.b;
+  auto& s_c = sh.c;
+  auto& s_y = sh.y;
+  const int tid = threadIdx.x;
   const int n_blk = ssm_blocks(a, CH);
-  const int seq = blockIdx.x / n_blk;
+  const int64_t id = blockIdx.x / n_blk;
   const SsmBlock blk(a, CH, blockIdx.x % n_blk);
-  int start, end;
-  seq_range(a.cu, seq, a.T, &start, &end);
+  int seq, piece, start, end;
+  if (!ssm_piece(a, split.seg, id, &seq, &piece, &start, &end)) return;
+  const int first = start + piece * (split.seg < end - start ? split.seg : 0);
+  const int last = min(end, (int)min((int64_t)first + split.seg, (int64_t)INT32_MAX));
+  const int tiles = (last - first + kTile - 1) / kTile;
+  // a pair of channels is 16 bytes; the order of a row's pairs is turned so
+  // that 8 helper lanes writing one each never meet on a bank
+  auto slot = [](int t, int c) {
+    if (L != 4) return c;
+    const int p = c >> 1, o = p >> 2;
+    return ((o << 2 | ((p ^ o ^ t) & 1) | ((p ^ o) & 2)) << 1) | (c & 1);
+  };
 
-  const IO* u = static_cast<const IO*>(a.u);
-  const IO* delta = static_cast<const IO*>(a.delta);
-  const IO* z = static_cast<const IO*>(a.z);
-  const IO* B = static_cast<const IO*>(a.B) + (int64_t)blk.g * a.b_group;
-  const IO* C = static_cast<const IO*>(a.C) + (int64_t)blk.g * a.c_group;
+  if (tid >= kSsmThreads) {
+    const int hid = tid - kSsmThreads;
+    const IO* u = static_cast<const IO*>(a.u) + blk.c0;
+    const IO* delta = static_cast<const IO*>(a.delta) + blk.c0;
+    const IO* z = a.z ? static_cast<const IO*>(a.z) + blk.c0 : nullptr;
+    const IO* dout = static_cast<const IO*>(save.d_out) + blk.c0;
+    const IO* B = static_cast<const IO*>(a.B) + (int64_t)blk.g * a.b_group;
+    const IO* C = static_cast<const IO*>(a.C) + (int64_t)blk.g * a.c_group;
+    IO* out = static_cast<IO*>(MODE == kSsmOut ? a.out : save.dz) + blk.c0;
+    const bool bc_vec = a.S % BN == 0 && a.b_stride % BN == 0 && a.c_stride % BN == 0 &&
+                        a.b_group % BN == 0 && a.c_group % BN == 0 &&
+                        (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C)) %
+                                alignof(Elems<IO, BN>) == 0;
+    // element j of this thread in a tile: VEC E neighbouring channels of one
+    // token, else one channel (or few) of E tokens
+    auto tok_of = [&](int j) { return VEC ? hid / TPT : (j * kHelpers + hid) / CH; };
+    auto ch_of = [&](int j) { return VEC ? hid % TPT * E + j : (j * kHelpers + hid) % CH; };
+    const int bt = hid / TPT, bn = hid % TPT * BN;
+    float bias[VEC ? E : 1], skip[VEC ? E : 1];
+#pragma unroll
+    for (int j = 0; j < (VEC ? E : 1); ++j) {
+      const int c = ch_of(j);
+      bias[j] = a.bias && c < blk.n ? a.bias[blk.c0 + c] : 0.f;
+      skip[j] = a.skip && c < blk.n ? a.skip[blk.c0 + c] : 0.f;
+    }
+    Elems<IO, E> ru, rd, rz, ro;
+    Elems<IO, BN> rb, rc;
+    auto load_e = [&](const IO* p, int64_t stride, int t0, int m, Elems<IO, E>& r) {
+      if (VEC) {
+        if (tok_of(0) < m && ch_of(0) < blk.n)
+          r = *reinterpret_cast<const Elems<IO, E>*>(p + (t0 + tok_of(0)) * stride + ch_of(0));
+        else
+          r = Elems<IO, E>{};
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          r.v[j] = tok_of(j) < m && ch_of(j) < blk.n ? p[(t0 + tok_of(j)) * stride + ch_of(j)]
+                                                     : IO(0.f);
+      }
+    };
+    auto load_bc = [&](const IO* p, int64_t stride, int t0, int m, Elems<IO, BN>& r) {
+      const IO* q = p + (int64_t)(t0 + bt) * stride + bn;
+      if (bc_vec) {
+        if (bt < m && bn < a.S)
+          r = *reinterpret_cast<const Elems<IO, BN>*>(q);
+        else
+          r = Elems<IO, BN>{};
+      } else {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) r.v[j] = bt < m && bn + j < a.S ? q[j] : IO(0.f);
+      }
+    };
+    auto load = [&](int i) {
+      const int t0 = first + i * kTile, m = min(kTile, last - t0);
+      load_e(delta, a.delta_stride, t0, m, rd);
+      load_e(u, a.u_stride, t0, m, ru);
+      load_bc(B, a.b_stride, t0, m, rb);
+      if (WANT_Y) {
+        load_bc(C, a.c_stride, t0, m, rc);
+        if (z) load_e(z, a.z_stride, t0, m, rz);
+      }
+      if (MODE == kSsmSaveDz) load_e(dout, a.D, t0, m, ro);
+    };
+    // what turns y into the result: (y + add) * mul, of the tile being
+    // converted and of the one before
+    float add[2][E], mul[2][E];
+    auto convert = [&](int i, float (&add_)[E], float (&mul_)[E]) {
+      const int t0 = first + i * kTile, m = min(kTile, last - t0), w = i & 1;
+      float dt[E], dtu[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float raw = to_f32(rd.v[j]) + bias[VEC ? j : 0], uu = to_f32(ru.v[j]);
+        const bool real = tok_of(j) < m && ch_of(j) < blk.n;
+        dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
+        dtu[j] = dt[j] * uu;
+        if (WANT_Y) {
+          add_[j] = skip[VEC ? j : 0] * uu;
+          float k = 1.f;
+          if (z) {
+            const float g = to_f32(rz.v[j]), s = sigmoid_f(g);
+            k = MODE == kSsmOut ? g * s : to_f32(ro.v[j]) * silu_grad(g, s);
+          }
+          mul_[j] = k;
+        }
+      }
+      if (VEC && E >= 2) {
+#pragma unroll
+        for (int j = 0; j < E; j += 2)
+          *reinterpret_cast<float4*>(&s_dt[w][tok_of(0)][slot(tok_of(0), ch_of(j))]) =
+              make_float4(dt[j], dtu[j], dt[j + 1], dtu[j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          s_dt[w][tok_of(j)][slot(tok_of(j), ch_of(j))] = make_float2(dt[j], dtu[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        s_b[w][bt][bn + j] = to_f32(rb.v[j]);
+        if (WANT_Y) s_c[w][bt][bn + j] = to_f32(rc.v[j]);
+      }
+    };
+    auto finish = [&](int i, const float (&add_)[E], const float (&mul_)[E]) {
+      const int t0 = first + i * kTile, m = min(kTile, last - t0), w = i & 1;
+      if (VEC) {
+        const int t = tok_of(0), c = ch_of(0);
+        if (t < m && c < blk.n) {
+          Elems<IO, E> r;
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            r.v[j] = from_f32<IO>((s_y[w][t][c + j] + add_[j]) * mul_[j]);
+          *reinterpret_cast<Elems<IO, E>*>(out + (int64_t)(t0 + t) * a.D + c) = r;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const int t = tok_of(j), c = ch_of(j);
+          if (t < m && c < blk.n)
+            out[(int64_t)(t0 + t) * a.D + c] = from_f32<IO>((s_y[w][t][c] + add_[j]) * mul_[j]);
+        }
+      }
+    };
+    if (tiles > 0) {
+      load(0);
+      convert(0, add[0], mul[0]);
+      if (tiles > 1) load(1);
+    }
+    __syncthreads();
+    for (int i = 0; i < tiles; i += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // tile i + k: parity k
+        if (i + k >= tiles) break;
+        if (WANT_Y && i + k > 0) finish(i + k - 1, add[1 - k], mul[1 - k]);
+        if (i + k + 1 < tiles) {
+          convert(i + k + 1, add[1 - k], mul[1 - k]);
+          if (i + k + 2 < tiles) load(i + k + 2);
+        }
+        __syncthreads();
+      }
+    }
+    if (WANT_Y && tiles > 0) {
+      if (tiles & 1)
+        finish(tiles - 1, add[0], mul[0]);
+      else
+        finish(tiles - 1, add[1], mul[1]);
+    }
+    return;
+  }
+
+  const int l = tid % L, ch = tid / L;
   const bool on = ch < blk.n;
-  const int d = blk.c0 + (on ? ch : 0);
+  const int d = blk.c0 + (on ? ch : 0), n0 = l * kSsmStates;
   float A2[kSsmStates], h[kSsmStates];
 #pragma unroll
   for (int i = 0; i < kSsmStates; ++i) {
-    const int n = l * kSsmStates + i;
-    const bool real = on && n < a.S;
-    A2[i] = real ? a.A[(int64_t)d * a.S + n] * kLog2e : 0.f;
-    h[i] = real && a.h0 ? a.h0[((int64_t)seq * a.D + d) * a.S + n] : 0.f;
+    const bool real = on && n0 + i < a.S;
+    A2[i] = real ? a.A[(int64_t)d * a.S + n0 + i] * kLog2e : 0.f;
+    h[i] = real && a.h0 && MODE != kSsmEnds ? a.h0[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
   }
-
-  for (int t0 = start; t0 < end; t0 += kTile) {
-    const int m = min(kTile, end - t0);
-    for (int i = tid; i < kTile * CH; i += kSsmThreads) {
-      const int t = i / CH, c = i % CH;
-      float2 v = make_float2(0.f, 0.f);
-      if (t < m && c < blk.n) {
-        const int64_t tok = t0 + t;
-        const float raw = to_f32(delta[tok * a.delta_stride + blk.c0 + c]) +
-                          (a.bias ? a.bias[blk.c0 + c] : 0.f);
-        v.x = a.softplus ? softplus_f(raw) : raw;
-        v.y = v.x * to_f32(u[tok * a.u_stride + blk.c0 + c]);
-      }
-      s_dt[t][c] = v;
-    }
-    for (int i = tid; i < kTile * SW; i += kSsmThreads) {
-      const int t = i / SW, n = i % SW;
-      const bool real = t < m && n < a.S;
-      s_b[t][n] = real ? to_f32(B[(int64_t)(t0 + t) * a.b_stride + n]) : 0.f;
-      s_c[t][n] = real ? to_f32(C[(int64_t)(t0 + t) * a.c_stride + n]) : 0.f;
-    }
-    __syncthreads();
-    for (int t = 0; t < m; t += 4) {
-      if (MODE == kSsmSave && t % kSsmChunk == 0) {
-        const int64_t id = ssm_chunk_id(seq, start, (t0 - start + t) / kSsmChunk);
+  if (MODE != kSsmEnds) {  // the ends of the segments before this one
+    for (int k = 0; k < piece; ++k) {
+      const int64_t row = (id - piece + k) * a.D + d;
+      const float sum = split.steps[row];
 #pragma unroll
-        for (int i = 0; i < kSsmStates; ++i)
-          if (on && l * kSsmStates + i < a.S)
-            save.states[(id * a.D + d) * a.S + l * kSsmStates + i] = h[i];
+      for (int i = 0; i < kSsmStates; ++i)
+        if (n0 + i < a.S)
+          h[i] = fmaf(ex2_f(sum * A2[i]), h[i], split.ends[row * a.S + n0 + i]);
+    }
+    if (!on)
+#pragma unroll
+      for (int i = 0; i < kSsmStates; ++i) h[i] = 0.f;
+  }
+  f32x2 h01 = pack2(h[0], h[1]), h23 = pack2(h[2], h[3]);
+  const f32x2 A01 = pack2(A2[0], A2[1]), A23 = pack2(A2[2], A2[3]);
+  float steps = 0.f;
+  const int slot0 = slot(0, ch), slot1 = slot(1, ch);
+  __syncthreads();
+  for (int i = 0; i < tiles; ++i) {
+    const int t0 = first + i * kTile, m = min(kTile, last - t0), w = i & 1;
+    for (int t = 0; t < m; t += 4) {
+      if ((MODE == kSsmSave || MODE == kSsmSaveDz) && t % kSsmChunk == 0) {
+        float* st = save.states +
+                    (ssm_piece_id(seq, start, kSsmChunk, (t0 - start + t) / kSsmChunk) * a.D + d) *
+                        a.S + n0;
+        float v[4];
+        unpack2(h01, v[0], v[1]);
+        unpack2(h23, v[2], v[3]);
+        if (a.S % 4 == 0) {
+          if (on && n0 < a.S) *reinterpret_cast<float4*>(st) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSsmStates; ++k)
+            if (on && n0 + k < a.S) st[k] = v[k];
+        }
       }
       float y[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         // behind the last token: step 0 keeps the state
-        const float2 v = s_dt[t + j][ch];
-        const float4 b = *reinterpret_cast<const float4*>(&s_b[t + j][l * kSsmStates]);
-        const float4 c = *reinterpret_cast<const float4*>(&s_c[t + j][l * kSsmStates]);
-        h[0] = fmaf(ex2_f(v.x * A2[0]), h[0], v.y * b.x);
-        h[1] = fmaf(ex2_f(v.x * A2[1]), h[1], v.y * b.y);
-        h[2] = fmaf(ex2_f(v.x * A2[2]), h[2], v.y * b.z);
-        h[3] = fmaf(ex2_f(v.x * A2[3]), h[3], v.y * b.w);
-        y[j] = fmaf(h[0], c.x, h[1] * c.y) + fmaf(h[2], c.z, h[3] * c.w);
+        const float2 v = s_dt[w][t + j][j & 1 ? slot1 : slot0];
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s_b[w][t + j][n0]);
+        const f32x2 dt = pack2(v.x, v.x), dtu = pack2(v.y, v.y);
+        float x0, x1, x2, x3;
+        unpack2(mul2(dt, A01), x0, x1);
+        unpack2(mul2(dt, A23), x2, x3);
+        h01 = fma2(pack2(ex2_f(x0), ex2_f(x1)), h01, mul2(dtu, b.x));
+        h23 = fma2(pack2(ex2_f(x2), ex2_f(x3)), h23, mul2(dtu, b.y));
+        if (WANT_Y) {
+          const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[w][t + j][n0]);
+          float lo, hi;
+          unpack2(fma2(h01, c.x, mul2(h23, c.y)), lo, hi);
+          y[j] = lo + hi;
+        }
+        if (MODE == kSsmEnds) steps += v.x;
       }
-      int first = 0;
-      SpreadSum<4, 1, L>::run(y, l, first);
-      constexpr int LEFT = L >= 4 ? 1 : 4 / L;
-      if (l < 4)
+      if (WANT_Y) {
+        int f = 0;
+        SpreadSum<4, 1, L>::run(y, l, f);
+        constexpr int LEFT = L >= 4 ? 1 : 4 / L;
+        if (l < 4)
 #pragma unroll
-        for (int j = 0; j < LEFT; ++j) s_y[t + first + j][ch] = y[j];
+          for (int j = 0; j < LEFT; ++j) s_y[w][t + f + j][ch] = y[j];
+      }
     }
     __syncthreads();
-    if (MODE == kSsmOut || save.dz) {
-      for (int i = tid; i < m * CH; i += kSsmThreads) {
-        const int t = i / CH, c = i % CH;
-        if (c >= blk.n) continue;
-        const int64_t tok = t0 + t;
-        const int dd = blk.c0 + c;
-        float y = s_y[t][c];
-        if (a.skip) y = fmaf(a.skip[dd], to_f32(u[tok * a.u_stride + dd]), y);
-        if (MODE == kSsmOut) {
-          if (z) {
-            const float g = to_f32(z[tok * a.z_stride + dd]);
-            y *= g * sigmoid_f(g);
-          }
-          static_cast<IO*>(a.out)[tok * a.D + dd] = from_f32<IO>(y);
-        } else {
-          const float g = to_f32(z[tok * a.z_stride + dd]);
-          const float dout = to_f32(static_cast<const IO*>(save.d_out)[tok * a.D + dd]);
-          static_cast<IO*>(save.dz)[tok * a.D + dd] =
-              from_f32<IO>(dout * y * silu_grad(g, sigmoid_f(g)));
-        }
-      }
-    }
   }
-  if (MODE == kSsmOut && a.h_out && on) {
+  unpack2(h01, h[0], h[1]);
+  unpack2(h23, h[2], h[3]);
+  float* fin = nullptr;
+  if (MODE == kSsmOut && a.h_out && last == end)
+    fin = a.h_out + ((int64_t)seq * a.D + d) * a.S + n0;
+  if (MODE == kSsmEnds) {
+    fin = split.ends + (id * a.D + d) * a.S + n0;
+    if (on && l == 0) split.steps[id * a.D + d] = steps;
+  }
+  if (fin && on) {
 #pragma unroll
     for (int i = 0; i < kSsmStates; ++i)
-      if (l * kSsmStates + i < a.S)
-        a.h_out[((int64_t)seq * a.D + d) * a.S + l * kSsmStates + i] = h[i];
+      if (n0 + i < a.S) fin[i] = h[i];
   }
 }
 
@@ -192,21 +383,45 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   }
 }
 
+// Whole vectors of E channels: aligned pointers and strides, and channel
+// blocks that start and end on them.
+template <typename IO, int E>
+bool vec_ok(const SsmArgs& a, const SsmSave& save) {
+  const void* ps[] = {a.u, a.delta, a.z, a.out, save.d_out, save.dz};
+  for (const void* p : ps)
+    if (p && !aligned_to(p, alignof(Elems<IO, E>))) return false;
+  return a.D / a.G % E == 0 && a.D % E == 0 && a.u_stride % E == 0 && a.delta_stride % E == 0 &&
+         a.z_stride % E == 0;
+}
+
+int64_t segments(const SsmArgs& a, int seg) { return a.tokens / seg + a.n_seqs + 1; }
+
 template <typename IO, int L, int MODE>
-cudaError_t fwd_launch(const SsmArgs& a, const SsmSave& save, cudaStream_t st) {
-  const unsigned grid = (unsigned)ssm_blocks(a, kSsmThreads / L) * (unsigned)a.n_seqs;
-  ssm_fwd_kernel<IO, L, MODE><<<grid, kSsmThreads, 0, st>>>(a, save);
+cudaError_t fwd_launch(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
+                       cudaStream_t st) {
+  const int64_t ids = split.seg == INT32_MAX ? a.n_seqs : segments(a, split.seg);
+  const unsigned grid = (unsigned)(ids * ssm_blocks(a, kSsmThreads / L));
+  constexpr int E = tile_of(L) * (kSsmThreads / L) / kHelpers;
+  auto* k = vec_ok<IO, E>(a, save) ? ssm_fwd_kernel<IO, L, MODE, true>
+                                   : ssm_fwd_kernel<IO, L, MODE, false>;
+  constexpr int bytes = sizeof(FwdShared<L, MODE == kSsmOut || MODE == kSsmSaveDz>);
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  k<<<grid, kSsmThreads + kHelpers, bytes, st>>>(a, save, split);
   return cudaGetLastError();
 }
 
 template <typename IO, int MODE>
-cudaError_t fwd_pick(const SsmArgs& a, const SsmSave& save, cudaStream_t st) {
+cudaError_t fwd_pick(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
+                     cudaStream_t st) {
   switch (ssm_lanes(a.S)) {
-    case 2: return fwd_launch<IO, 2, MODE>(a, save, st);
-    case 4: return fwd_launch<IO, 4, MODE>(a, save, st);
-    case 8: return fwd_launch<IO, 8, MODE>(a, save, st);
-    case 16: return fwd_launch<IO, 16, MODE>(a, save, st);
-    case 32: return fwd_launch<IO, 32, MODE>(a, save, st);
+    case 2: return fwd_launch<IO, 2, MODE>(a, save, split, st);
+    case 4: return fwd_launch<IO, 4, MODE>(a, save, split, st);
+    case 8: return fwd_launch<IO, 8, MODE>(a, save, split, st);
+    case 16: return fwd_launch<IO, 16, MODE>(a, save, split, st);
+    case 32: return fwd_launch<IO, 32, MODE>(a, save, split, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -232,17 +447,37 @@ cudaError_t step_pick(const SsmArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t st) {
-  if (a.n_seqs == 0) return cudaSuccess;
-  const SsmSave none{};
-  return a.bf16 ? fwd_pick<__nv_bfloat16, kSsmOut>(a, none, st)
-                : fwd_pick<float, kSsmOut>(a, none, st);
+size_t ssm_split_bytes(const SsmArgs& a, int seg) {
+  if (seg == INT32_MAX) return 0;
+  return (size_t)segments(a, seg) * a.D * (a.S + 1) * sizeof(float);
 }
 
-cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, cudaStream_t st) {
+namespace {
+template <typename IO>
+cudaError_t ends_pass(const SsmArgs& a, const SsmSplit& split, cudaStream_t st) {
+  return split.seg == INT32_MAX ? cudaSuccess
+                                : fwd_pick<IO, kSsmEnds>(a, SsmSave{}, split, st);
+}
+template <typename IO>
+cudaError_t scan(const SsmArgs& a, const SsmSave* save, const SsmSplit& split, cudaStream_t st) {
+  cudaError_t e = ends_pass<IO>(a, split, st);
+  if (e != cudaSuccess) return e;
+  if (!save) return fwd_pick<IO, kSsmOut>(a, SsmSave{}, split, st);
+  return save->dz ? fwd_pick<IO, kSsmSaveDz>(a, *save, split, st)
+                  : fwd_pick<IO, kSsmSave>(a, *save, split, st);
+}
+}  // namespace
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t st) {
   if (a.n_seqs == 0) return cudaSuccess;
-  return a.bf16 ? fwd_pick<__nv_bfloat16, kSsmSave>(a, save, st)
-                : fwd_pick<float, kSsmSave>(a, save, st);
+  const SsmSplit whole{INT32_MAX, nullptr, nullptr};
+  return a.bf16 ? scan<__nv_bfloat16>(a, nullptr, whole, st) : scan<float>(a, nullptr, whole, st);
+}
+
+cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
+                            cudaStream_t st) {
+  if (a.n_seqs == 0) return cudaSuccess;
+  return a.bf16 ? scan<__nv_bfloat16>(a, &save, split, st) : scan<float>(a, &save, split, st);
 }
 
 cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t st) {

@@ -6,10 +6,10 @@
 //   h_t[n] = a_t[n] h_{t-1}[n] + step_t u_t B_t[n];  y_t = sum_n C_t[n] h_t[n]
 //
 // A lane owns 4 states of one channel; L lanes hold a channel's states
-// (4 L >= S, absent states have A = B = C = 0 and stay 0), a CTA of 128
-// threads holds 128 / L channels of one group and one sequence and walks the
-// sequence in tiles of tokens.  Per (token, channel) a tile keeps step and
-// step * u, per token the 4 L values of B and of C, all fp32 in shared memory.
+// (4 L >= S, absent states have A = B = C = 0 and stay 0), 128 threads hold
+// 128 / L channels of one group and one sequence and walk the sequence in
+// tiles of tokens.  Per (token, channel) a tile keeps step and step * u, per
+// token the 4 L values of B and of C, all fp32 in shared memory.
 #pragma once
 
 #include "kda_layer.cuh"
@@ -68,26 +68,61 @@ struct SpreadSum {  // lanes LOW, 2 LOW, ... < HIGH
   }
 };
 
-// Chunk ids of the backward's saved states: chunk c (of 8 tokens) of sequence
-// s has id start_s / 8 + s + c.  The ids of two sequences never meet, since
-// floor((start + len) / 8) + 1 >= floor(start / 8) + ceil(len / 8), and are
-// below tokens / 8 + n_seqs + 1.
+// Pieces of n tokens of every sequence (the backward's saved states every 8
+// tokens; the segments of a split scan): piece c of sequence s has the id
+// start_s / n + s + c.  A sequence has max(1, ceil(len / n)) pieces; the ids of
+// two sequences never meet, since floor((start + len) / n) + 1 >=
+// floor(start / n) + max(1, ceil(len / n)), and are below tokens / n + n_seqs
+// + 1.
+__host__ __device__ __forceinline__ int64_t ssm_piece_id(int s, int start, int n, int c) {
+  return (int64_t)(start / n) + s + c;
+}
 constexpr int kSsmChunk = 8;
-__host__ __device__ __forceinline__ int64_t ssm_chunk_id(int s, int start, int c) {
-  return (int64_t)(start / kSsmChunk) + s + c;
+
+// The sequence and piece of an id; false where the id has none.
+__device__ __forceinline__ bool ssm_piece(const SsmArgs& a, int n, int64_t id, int* seq, int* c,
+                                          int* start, int* end) {
+  int lo = 0, hi = a.n_seqs;  // the last sequence whose first id is <= id
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    int s, e;
+    seq_range(a.cu, mid, a.T, &s, &e);
+    if (ssm_piece_id(mid, s, n, 0) <= id)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  seq_range(a.cu, lo, a.T, start, end);
+  const int64_t k = id - ssm_piece_id(lo, *start, n, 0);
+  const int len = *end - *start;
+  *seq = lo;
+  *c = (int)k;
+  return k >= 0 && k < max((int64_t)1, ((int64_t)len + n - 1) / n);
 }
 
-// What the forward kernel does with a token's result.
+// What one pass of the forward kernel is for.
 enum SsmMode {
-  kSsmOut,   // out = y silu(z)
-  kSsmSave,  // backward's first pass: saved states, and dz = d_out y silu'(z)
+  kSsmOut,     // out = y silu(z), final states
+  kSsmSave,    // the backward's first pass: the state at every 8th token
+  kSsmSaveDz,  // the same, and dz = d_out y silu'(z)
+  kSsmEnds,    // a split scan's first pass: each segment's end from state 0
+};
+// A split scan: segments of `seg` tokens; ends [segment id][D][S] their states
+// from zero, steps [segment id][D] their sums of steps (a segment's decay is
+// exp(A * sum of steps)).
+struct SsmSplit {
+  int seg;  // INT32_MAX: not split
+  float* ends;
+  float* steps;
 };
 struct SsmSave {
-  float* states;      // [chunk ids][D][S]
+  float* states;      // [piece ids of 8 tokens][D][S]
   const void* d_out;  // for dz
-  void* dz;           // or null
+  void* dz;
 };
-cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, cudaStream_t stream);
+size_t ssm_split_bytes(const SsmArgs& a, int seg);
+cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
+                            cudaStream_t stream);
 
 // Lanes per channel for S states: the smallest power of two >= S / 4, at
 // least 2 (so that a CTA never holds more than 64 channels).

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_bwd_kernel(SsmBwdArgs b, BwdP
       s_c[t][n] = real ? to_f32(C[(int64_t)(t0 + t) * a.c_stride + n]) : 0.f;
     }
     float hp[K + 1][kSsmStates], av[K][kSsmStates];
-    const float* hs = part.states + (ssm_chunk_id(seq, start, k) * a.D + d) * a.S;
+    const float* hs = part.states + (ssm_piece_id(seq, start, K, k) * a.D + d) * a.S;
 #pragma unroll
     for (int i = 0; i < kSsmStates; ++i)
       hp[0][i] = on && l * kSsmStates + i < a.S ? hs[l * kSsmStates + i] : 0.f;
@@ -298,7 +298,8 @@ cudaError_t launch_ssm_bwd(const SsmBwdArgs& b, void* ws, cudaStream_t st) {
                 reinterpret_cast<float*>(w + o.dA), reinterpret_cast<float*>(w + o.dskip),
                 reinterpret_cast<float*>(w + o.dbias)};
   SsmSave save{part.states, b.d_out, b.f.z ? b.dz : nullptr};
-  cudaError_t e = launch_ssm_save(b.f, save, st);
+  const SsmSplit whole{INT32_MAX, nullptr, nullptr};
+  cudaError_t e = launch_ssm_save(b.f, save, whole, st);
   if (e == cudaSuccess)
     e = b.f.bf16 ? bwd_pick<__nv_bfloat16>(b, part, st) : bwd_pick<float>(b, part, st);
   if (e == cudaSuccess) e = seq_sum(part.dA, b.f, (int64_t)b.f.D * b.f.S, b.dA, st);
