@@ -18,11 +18,15 @@ struct Raw;  // storage of VEC elements
 template <>
 struct Raw<__nv_bfloat16, 1> { uint16_t r; };
 template <>
+struct Raw<__nv_bfloat16, 2> { uint32_t r; };
+template <>
 struct Raw<__nv_bfloat16, 4> { uint2 r; };
 template <>
 struct Raw<__nv_bfloat16, 8> { uint4 r; };
 template <>
 struct Raw<float, 1> { float r; };
+template <>
+struct Raw<float, 2> { float2 r; };
 template <>
 struct Raw<float, 4> { float4 r; };
 template <>
@@ -61,6 +65,12 @@ __device__ __forceinline__ uint32_t bf_pair(float lo, float hi) {
 __device__ __forceinline__ void pack(const float (&v)[1], Raw<__nv_bfloat16, 1>& a) {
   const __nv_bfloat16 b = __float2bfloat16_rn(v[0]);
   a.r = *reinterpret_cast<const uint16_t*>(&b);
+}
+__device__ __forceinline__ void pack(const float (&v)[2], Raw<__nv_bfloat16, 2>& a) {
+  a.r = bf_pair(v[0], v[1]);
+}
+__device__ __forceinline__ void pack(const float (&v)[2], Raw<float, 2>& a) {
+  a.r = make_float2(v[0], v[1]);
 }
 __device__ __forceinline__ void pack(const float (&v)[4], Raw<__nv_bfloat16, 4>& a) {
   a.r = make_uint2(bf_pair(v[0], v[1]), bf_pair(v[2], v[3]));

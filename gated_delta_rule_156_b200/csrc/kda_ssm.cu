@@ -29,10 +29,52 @@ struct FwdShared {
   float y[2][WANT_Y ? TILE : 1][YP];
 };
 
-// N consecutive elements in one access where VEC, else one by one.
-template <typename IO, int N>
-struct __align__(N * sizeof(IO) >= 16 ? 16 : N * sizeof(IO)) Elems {
-  IO v[N];
+// N elements on their way from memory, as the 32-bit registers that the loads
+// write: nothing touches them before get(), so that every load of a tile is
+// in flight at once.  VEC: neighbouring elements, aligned to their whole size
+// (16 bytes at most), else one register each.
+template <typename IO, int N, bool VEC>
+struct Held {
+  static constexpr int BYTES = N * (int)sizeof(IO);
+  static constexpr bool PACKED = VEC && BYTES % 4 == 0;
+  static constexpr int WORDS = PACKED ? BYTES / 4 : N;
+  static constexpr int ALIGN = VEC ? (BYTES > 16 ? 16 : BYTES) : (int)sizeof(IO);
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void one(int j, const IO* p) {
+    if constexpr (sizeof(IO) == 2)
+      w[j] = *reinterpret_cast<const uint16_t*>(p);
+    else
+      w[j] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void all(const IO* p) {
+    if constexpr (!PACKED) {
+      one(0, p);
+    } else if constexpr (WORDS == 1) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (WORDS == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = v.x;
+        w[i + 1] = v.y;
+        w[i + 2] = v.z;
+        w[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[j]);
+    if constexpr (!PACKED) return __uint_as_float(w[j] << 16);
+    return j & 1 ? bf_hi(w[j / 2]) : bf_lo(w[j / 2]);
+  }
 };
 
 // CTA: 4 warps run the recurrence, 4 helper warps feed them and finish their
@@ -86,7 +128,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     const bool bc_vec = a.S % BN == 0 && a.b_stride % BN == 0 && a.c_stride % BN == 0 &&
                         a.b_group % BN == 0 && a.c_group % BN == 0 &&
                         (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C)) %
-                                alignof(Elems<IO, BN>) == 0;
+                                Held<IO, BN, true>::ALIGN == 0;
     // element j of this thread in a tile: VEC E neighbouring channels of one
     // token, else one channel (or few) of E tokens
     auto tok_of = [&](int j) { return VEC ? hid / TPT : (j * kHelpers + hid) / CH; };
@@ -99,40 +141,50 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       bias[j] = a.bias && c < blk.n ? a.bias[blk.c0 + c] : 0.f;
       skip[j] = a.skip && c < blk.n ? a.skip[blk.c0 + c] : 0.f;
     }
-    Elems<IO, E> ru, rd, rz, ro;
-    Elems<IO, BN> rb, rc;
-    auto load_e = [&](const IO* p, int64_t stride, int t0, int m, Elems<IO, E>& r) {
+    Held<IO, E, VEC> ru, rd, rz, ro;
+    Held<IO, BN, true> rb, rc;   // bc_vec, and fp32 either way
+    Held<IO, BN, false> sb, sc;  // bf16 otherwise
+    constexpr bool ONE = sizeof(IO) == 4;
+    auto load_e = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, E, VEC>& r) {
+      r.clear();
       if (VEC) {
         if (tok_of(0) < m && ch_of(0) < blk.n)
-          r = *reinterpret_cast<const Elems<IO, E>*>(p + (t0 + tok_of(0)) * stride + ch_of(0));
-        else
-          r = Elems<IO, E>{};
+          r.all(p + (t0 + tok_of(0)) * stride + ch_of(0));
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          r.v[j] = tok_of(j) < m && ch_of(j) < blk.n ? p[(t0 + tok_of(j)) * stride + ch_of(j)]
-                                                     : IO(0.f);
+          if (tok_of(j) < m && ch_of(j) < blk.n)
+            r.one(j, p + (t0 + tok_of(j)) * stride + ch_of(j));
       }
     };
-    auto load_bc = [&](const IO* p, int64_t stride, int t0, int m, Elems<IO, BN>& r) {
+    auto load_bc = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, BN, true>& r,
+                       Held<IO, BN, false>& s) {
       const IO* q = p + (int64_t)(t0 + bt) * stride + bn;
       if (bc_vec) {
-        if (bt < m && bn < a.S)
-          r = *reinterpret_cast<const Elems<IO, BN>*>(q);
-        else
-          r = Elems<IO, BN>{};
+        r.clear();
+        if (bt < m && bn < a.S) r.all(q);
       } else {
+        if (ONE)
+          r.clear();
+        else
+          s.clear();
 #pragma unroll
-        for (int j = 0; j < BN; ++j) r.v[j] = bt < m && bn + j < a.S ? q[j] : IO(0.f);
+        for (int j = 0; j < BN; ++j)
+          if (bt < m && bn + j < a.S) {
+            if (ONE)
+              r.one(j, q + j);
+            else
+              s.one(j, q + j);
+          }
       }
     };
     auto load = [&](int i) {
       const int t0 = first + i * kTile, m = min(kTile, last - t0);
       load_e(delta, a.delta_stride, t0, m, rd);
       load_e(u, a.u_stride, t0, m, ru);
-      load_bc(B, a.b_stride, t0, m, rb);
+      load_bc(B, a.b_stride, t0, m, rb, sb);
       if (WANT_Y) {
-        load_bc(C, a.c_stride, t0, m, rc);
+        load_bc(C, a.c_stride, t0, m, rc, sc);
         if (z) load_e(z, a.z_stride, t0, m, rz);
       }
       if (MODE == kSsmSaveDz) load_e(dout, a.D, t0, m, ro);
@@ -145,7 +197,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       float dt[E], dtu[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float raw = to_f32(rd.v[j]) + bias[VEC ? j : 0], uu = to_f32(ru.v[j]);
+        const float raw = rd.get(j) + bias[VEC ? j : 0], uu = ru.get(j);
         const bool real = tok_of(j) < m && ch_of(j) < blk.n;
         dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
         dtu[j] = dt[j] * uu;
@@ -153,8 +205,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           add_[j] = skip[VEC ? j : 0] * uu;
           float k = 1.f;
           if (z) {
-            const float g = to_f32(rz.v[j]), s = sigmoid_f(g);
-            k = MODE == kSsmOut ? g * s : to_f32(ro.v[j]) * silu_grad(g, s);
+            const float g = rz.get(j), s = sigmoid_f(g);
+            k = MODE == kSsmOut ? g * s : ro.get(j) * silu_grad(g, s);
           }
           mul_[j] = k;
         }
@@ -171,8 +223,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       }
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        s_b[w][bt][bn + j] = to_f32(rb.v[j]);
-        if (WANT_Y) s_c[w][bt][bn + j] = to_f32(rc.v[j]);
+        s_b[w][bt][bn + j] = ONE || bc_vec ? rb.get(j) : sb.get(j);
+        if (WANT_Y) s_c[w][bt][bn + j] = ONE || bc_vec ? rc.get(j) : sc.get(j);
       }
     };
     auto finish = [&](int i, const float (&add_)[E], const float (&mul_)[E]) {
@@ -180,11 +232,10 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       if (VEC) {
         const int t = tok_of(0), c = ch_of(0);
         if (t < m && c < blk.n) {
-          Elems<IO, E> r;
+          float r[E];
 #pragma unroll
-          for (int j = 0; j < E; ++j)
-            r.v[j] = from_f32<IO>((s_y[w][t][c + j] + add_[j]) * mul_[j]);
-          *reinterpret_cast<Elems<IO, E>*>(out + (int64_t)(t0 + t) * a.D + c) = r;
+          for (int j = 0; j < E; ++j) r[j] = (s_y[w][t][c + j] + add_[j]) * mul_[j];
+          store_vec<IO, E>(out + (int64_t)(t0 + t) * a.D + c, r);
         }
       } else {
 #pragma unroll
@@ -222,7 +273,11 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     return;
   }
 
-  const int l = tid % L, ch = tid / L;
+  // a warp's channels in the low lane bits, the groups of 4 states in the high
+  // ones: neighbouring lanes then share the words of B and C, which a 16-byte
+  // shared load serves in two wavefronts (four the other way round)
+  constexpr int CW = 32 / L;  // channels a warp
+  const int lane = tid % 32, l = lane / CW, ch = tid / 32 * CW + lane % CW;
   const bool on = ch < blk.n;
   const int d = blk.c0 + (on ? ch : 0), n0 = l * kSsmStates;
   float A2[kSsmStates], h[kSsmStates];
@@ -268,29 +323,38 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
             if (on && n0 + k < a.S) st[k] = v[k];
         }
       }
-      float y[4];
+      // the decays and inputs of four tokens, then the recurrence through them
+      f32x2 e01[4], e23[4], x01[4], x23[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         // behind the last token: step 0 keeps the state
         const float2 v = s_dt[w][t + j][j & 1 ? slot1 : slot0];
         const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s_b[w][t + j][n0]);
         const f32x2 dt = pack2(v.x, v.x), dtu = pack2(v.y, v.y);
-        float x0, x1, x2, x3;
-        unpack2(mul2(dt, A01), x0, x1);
-        unpack2(mul2(dt, A23), x2, x3);
-        h01 = fma2(pack2(ex2_f(x0), ex2_f(x1)), h01, mul2(dtu, b.x));
-        h23 = fma2(pack2(ex2_f(x2), ex2_f(x3)), h23, mul2(dtu, b.y));
+        float p[4];
+        unpack2(mul2(dt, A01), p[0], p[1]);
+        unpack2(mul2(dt, A23), p[2], p[3]);
+        e01[j] = pack2(ex2_f(p[0]), ex2_f(p[1]));
+        e23[j] = pack2(ex2_f(p[2]), ex2_f(p[3]));
+        x01[j] = mul2(dtu, b.x);
+        x23[j] = mul2(dtu, b.y);
+        if (MODE == kSsmEnds) steps += v.x;
+      }
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h01 = fma2(e01[j], h01, x01[j]);
+        h23 = fma2(e23[j], h23, x23[j]);
         if (WANT_Y) {
           const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[w][t + j][n0]);
           float lo, hi;
           unpack2(fma2(h01, c.x, mul2(h23, c.y)), lo, hi);
           y[j] = lo + hi;
         }
-        if (MODE == kSsmEnds) steps += v.x;
       }
       if (WANT_Y) {
         int f = 0;
-        SpreadSum<4, 1, L>::run(y, l, f);
+        SpreadSum<4, CW, 32>::run(y, lane, f);
         constexpr int LEFT = L >= 4 ? 1 : 4 / L;
         if (l < 4)
 #pragma unroll
@@ -389,7 +453,7 @@ template <typename IO, int E>
 bool vec_ok(const SsmArgs& a, const SsmSave& save) {
   const void* ps[] = {a.u, a.delta, a.z, a.out, save.d_out, save.dz};
   for (const void* p : ps)
-    if (p && !aligned_to(p, alignof(Elems<IO, E>))) return false;
+    if (p && !aligned_to(p, Held<IO, E, true>::ALIGN)) return false;
   return a.D / a.G % E == 0 && a.D % E == 0 && a.u_stride % E == 0 && a.delta_stride % E == 0 &&
          a.z_stride % E == 0;
 }
