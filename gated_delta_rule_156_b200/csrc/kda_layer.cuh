@@ -99,8 +99,20 @@ __device__ __forceinline__ void store_vec(IO* p, const float (&v)[VEC]) {
   *reinterpret_cast<Raw<IO, VEC>*>(p) = a;
 }
 
+// 2^x and 1 / x, to 2 and 1 units of 2^-23; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid_f(float x) {
-  return __fdividef(1.f, 1.f + __expf(-x));
+  return rcp_f(1.f + ex2_f(-kLog2e * x));
 }
 // d silu(x) / dx from x and s = sigmoid(x)
 __device__ __forceinline__ float silu_grad(float x, float s) {
@@ -111,8 +123,8 @@ __device__ __forceinline__ float silu_grad(float x, float s) {
 // terms leave 2e-8 of the value, for the smallest steps too (a logarithm of
 // 1 + e would lose them).
 __device__ __forceinline__ float softplus_f(float x) {
-  const float e = __expf(-fabsf(x));
-  const float s = __fdividef(e, 2.f + e), q = s * s;
+  const float e = ex2_f(-kLog2e * fabsf(x));
+  const float s = e * rcp_f(2.f + e), q = s * s;
   float p = 1.f / 13.f;
   p = fmaf(p, q, 1.f / 11.f);
   p = fmaf(p, q, 1.f / 9.f);

@@ -13,6 +13,8 @@ namespace kda {
 namespace {
 
 constexpr int kHelpers = 128;  // helper threads
+constexpr int kGroup = 8;      // tokens the recurrence takes at a time
+static_assert(kGroup == kSsmChunk, "a saved state per group");
 
 // Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
 // (a helper then holds 8 pairs as with four lanes, and nothing spills).
@@ -307,8 +309,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   __syncthreads();
   for (int i = 0; i < tiles; ++i) {
     const int t0 = first + i * kTile, m = min(kTile, last - t0), w = i & 1;
-    for (int t = 0; t < m; t += 4) {
-      if ((MODE == kSsmSave || MODE == kSsmSaveDz) && t % kSsmChunk == 0) {
+    for (int t = 0; t < m; t += kGroup) {
+      if (MODE == kSsmSave || MODE == kSsmSaveDz) {
         float* st = save.states +
                     (ssm_piece_id(seq, start, kSsmChunk, (t0 - start + t) / kSsmChunk) * a.D + d) *
                         a.S + n0;
@@ -323,10 +325,11 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
             if (on && n0 + k < a.S) st[k] = v[k];
         }
       }
-      // the decays and inputs of four tokens, then the recurrence through them
-      f32x2 e01[4], e23[4], x01[4], x23[4];
+      // the decays and inputs of 8 tokens, then the recurrence through them:
+      // 32 exponentials in a row cover the latency of the rest
+      f32x2 e01[kGroup], e23[kGroup], x01[kGroup], x23[kGroup];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kGroup; ++j) {
         // behind the last token: step 0 keeps the state
         const float2 v = s_dt[w][t + j][j & 1 ? slot1 : slot0];
         const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s_b[w][t + j][n0]);
@@ -340,25 +343,28 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         x23[j] = mul2(dtu, b.y);
         if (MODE == kSsmEnds) steps += v.x;
       }
-      float y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h01 = fma2(e01[j], h01, x01[j]);
-        h23 = fma2(e23[j], h23, x23[j]);
-        if (WANT_Y) {
-          const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[w][t + j][n0]);
-          float lo, hi;
-          unpack2(fma2(h01, c.x, mul2(h23, c.y)), lo, hi);
-          y[j] = lo + hi;
+      for (int q = 0; q < kGroup; q += 4) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h01 = fma2(e01[q + j], h01, x01[q + j]);
+          h23 = fma2(e23[q + j], h23, x23[q + j]);
+          if (WANT_Y) {
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[w][t + q + j][n0]);
+            float lo, hi;
+            unpack2(fma2(h01, c.x, mul2(h23, c.y)), lo, hi);
+            y[j] = lo + hi;
+          }
         }
-      }
-      if (WANT_Y) {
-        int f = 0;
-        SpreadSum<4, CW, 32>::run(y, lane, f);
-        constexpr int LEFT = L >= 4 ? 1 : 4 / L;
-        if (l < 4)
+        if (WANT_Y) {
+          int f = 0;
+          SpreadSum<4, CW, 32>::run(y, lane, f);
+          constexpr int LEFT = L >= 4 ? 1 : 4 / L;
+          if (l < 4)
 #pragma unroll
-          for (int j = 0; j < LEFT; ++j) s_y[w][t + f + j][ch] = y[j];
+            for (int j = 0; j < LEFT; ++j) s_y[w][t + q + f + j][ch] = y[j];
+        }
       }
     }
     __syncthreads();

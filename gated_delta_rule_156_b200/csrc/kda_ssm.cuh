@@ -18,14 +18,6 @@ namespace kda {
 
 constexpr int kSsmThreads = 128;
 constexpr int kSsmStates = 4;  // states per lane
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2_f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The channels of a CTA: channel blocks are counted group by group.
 struct SsmBlock {
   int g, c0, n;  // group, first channel, channels (<= CH)
