@@ -19,6 +19,19 @@ kda_status done(cudaError_t e) {
   return KDA_ERR_CUDA;
 }
 
+// Runs `launch` with stream-ordered workspace.
+template <typename F>
+kda_status with_workspace(size_t bytes, cudaStream_t stream, F launch) {
+  void* ws = nullptr;
+  cudaError_t e = kda::api_take_workspace(bytes, stream, &ws);
+  if (e == cudaSuccess) e = launch(ws);
+  if (ws) {
+    const cudaError_t f = cudaFreeAsync(ws, stream);
+    if (e == cudaSuccess) e = f;
+  }
+  return done(e);
+}
+
 // The memory of one argument.
 struct Span {
   const void* p;
@@ -123,9 +136,10 @@ kda_status ssm_args(const kda_ssm_shape* s, bool packed, kda::SsmArgs* a) {
   if (a->b_stride < bw || a->c_stride < cw || a->b_stride > ((int64_t)1 << 40) ||
       a->c_stride > ((int64_t)1 << 40))
     return KDA_ERR_INVALID_ARG;
-  // CTAs and the backward's sums are counted in 31 bits
+  // CTAs (of segments of 128 tokens at the least, where a scan is split) and
+  // the backward's sums are counted in 31 bits
   const int ch = kda::kSsmThreads / kda::ssm_lanes(s->S);
-  if ((int64_t)kda::ssm_blocks(*a, ch) * a->n_seqs > INT32_MAX ||
+  if ((int64_t)kda::ssm_blocks(*a, ch) * (a->n_seqs + a->tokens / 128 + 1) > INT32_MAX ||
       a->tokens * s->G * s->S > ((int64_t)1 << 38) ||
       (int64_t)a->n_seqs * s->D > ((int64_t)1 << 33))
     return KDA_ERR_UNSUPPORTED;
@@ -237,14 +251,8 @@ kda_status kda_short_conv_bwd(const kda_conv_shape* shape, const void* x, const 
   a.dw = d_weight;
   a.db = d_bias;
   a.d_past = d_initial_state;
-  void* ws = nullptr;
-  cudaError_t ce = kda::api_take_workspace(kda::conv_bwd_workspace_bytes(a), stream, &ws);
-  if (ce == cudaSuccess) ce = kda::launch_conv_bwd(a, ws, stream);
-  if (ws) {
-    const cudaError_t f = cudaFreeAsync(ws, stream);
-    if (ce == cudaSuccess) ce = f;
-  }
-  return done(ce);
+  return with_workspace(kda::conv_bwd_workspace_bytes(a), stream,
+                        [&](void* ws) { return kda::launch_conv_bwd(a, ws, stream); });
 }
 
 kda_status kda_short_conv_step(const kda_conv_shape* shape, const void* x, const float* weight,
@@ -298,7 +306,9 @@ kda_status kda_ssm_scan_fwd(const kda_ssm_shape* shape, const void* u, const voi
   const bool same = final_state && final_state == initial_state;
   const Span outs[] = {so, sf};
   if ((st = check_memory(in, same ? 9 : 10, outs, 2)) != KDA_OK) return st;
-  return done(kda::launch_ssm_fwd(a, stream));
+  const int sms = kda::sm_count();
+  return with_workspace(kda::ssm_fwd_workspace_bytes(a, sms), stream,
+                        [&](void* ws) { return kda::launch_ssm_fwd(a, ws, sms, stream); });
 }
 
 static kda_status ssm_bwd_args(const kda_ssm_shape* shape, bool packed, kda::SsmBwdArgs* b) {
@@ -354,14 +364,8 @@ kda_status kda_ssm_scan_bwd(const kda_ssm_shape* shape, const void* u, const voi
                        flat(d_skip, a.D, 4), flat(dz, a.tokens * a.D, e),
                        flat(d_delta_bias, a.D, 4), flat(d_initial_state, state, 4)};
   if ((st = check_memory(in, 12, outs, 9)) != KDA_OK) return st;
-  void* ws = nullptr;
-  cudaError_t ce = kda::api_take_workspace(kda::ssm_bwd_workspace_bytes(b), stream, &ws);
-  if (ce == cudaSuccess) ce = kda::launch_ssm_bwd(b, ws, stream);
-  if (ws) {
-    const cudaError_t f = cudaFreeAsync(ws, stream);
-    if (ce == cudaSuccess) ce = f;
-  }
-  return done(ce);
+  return with_workspace(kda::ssm_bwd_workspace_bytes(b), stream,
+                        [&](void* ws) { return kda::launch_ssm_bwd(b, ws, stream); });
 }
 
 kda_status kda_ssm_scan_bwd_plan(const kda_ssm_shape* shape, int packed, int* kernels,
@@ -472,15 +476,9 @@ kda_status kda_block_norm_bwd(const kda_norm_shape* shape, const void* x,
   a.dpost = d_post_weight;
   a.dscale = d_scale;
   a.dpre = d_pre_weight;
-  void* ws = nullptr;
   const int sms = kda::sm_count();
-  cudaError_t ce = kda::api_take_workspace(kda::norm_bwd_workspace_bytes(a, sms), stream, &ws);
-  if (ce == cudaSuccess) ce = kda::launch_norm_bwd(a, ws, sms, stream);
-  if (ws) {
-    const cudaError_t f = cudaFreeAsync(ws, stream);
-    if (ce == cudaSuccess) ce = f;
-  }
-  return done(ce);
+  return with_workspace(kda::norm_bwd_workspace_bytes(a, sms), stream,
+                        [&](void* ws) { return kda::launch_norm_bwd(a, ws, sms, stream); });
 }
 
 }  // extern "C"

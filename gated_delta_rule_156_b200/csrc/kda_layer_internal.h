@@ -62,7 +62,9 @@ struct SsmArgs {
   int64_t tokens, u_stride, delta_stride, z_stride, b_stride, b_group, c_stride, c_group;
   bool bf16, softplus;
 };
-cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t stream);
+// The scan of long sequences with few CTAs runs split (sms: the device's SMs).
+size_t ssm_fwd_workspace_bytes(const SsmArgs& a, int sms);
+cudaError_t launch_ssm_fwd(const SsmArgs& a, void* workspace, int sms, cudaStream_t stream);
 cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t stream);
 struct SsmBwdArgs {
   SsmArgs f;

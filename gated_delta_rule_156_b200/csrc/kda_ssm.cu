@@ -12,7 +12,8 @@ namespace kda {
 
 namespace {
 
-constexpr int kHelpers = 128;  // helper threads
+constexpr int kHelpers = 128;     // helper threads
+constexpr int kMinSegment = 128;  // tokens: below, a split's passes are all latency
 
 // Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
 // (a helper then holds 8 pairs as with four lanes, and nothing spills).
@@ -79,9 +80,9 @@ struct Held {
 
 // CTA: 4 warps run the recurrence, 4 helper warps feed them and finish their
 // results, tile by tile of 32 tokens with one barrier a tile: while the
-// recurrence runs tile i, the helpers turn tile i + 1 into step, step * u, B
-// and C (its loads were issued a tile earlier and wait in registers), finish
-// and store tile i - 1, and issue the loads of tile i + 2.  A helper thread
+// recurrence runs tile i, the helpers finish and store tile i - 1, turn tile
+// i + 1 (its loads were issued a tile earlier and wait in registers) into
+// step, step * u, B and C, and issue the loads of tile i + 2.  A helper thread
 // keeps what a token's result needs besides y (skip * u, silu(z)) in
 // registers, since it stores the same elements it loaded.
 template <typename IO, int L, int MODE, bool VEC>
@@ -92,7 +93,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   constexpr int CH = Shared::CH, SW = Shared::SW, kTile = Shared::TILE;
   constexpr int E = kTile * CH / kHelpers;   // (token, channel) pairs a helper
   constexpr int BN = kTile * SW / kHelpers;  // values of B (and of C) a helper
-  constexpr int TPT = kHelpers / kTile;      // helpers a token
+  constexpr int TPT = kHelpers / kTile;      // helpers a token (VEC)
+  constexpr int TSTEP = kHelpers / CH;       // tokens between two of a helper's (not VEC)
   extern __shared__ __align__(16) unsigned char s_raw[];
   Shared& sh = *reinterpret_cast<Shared*>(s_raw);
   auto& s_dt = sh.dt;
@@ -107,7 +109,11 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   if (!ssm_piece(a, split.seg, id, &seq, &piece, &start, &end)) return;
   const int first = start + piece * (split.seg < end - start ? split.seg : 0);
   const int last = min(end, (int)min((int64_t)first + split.seg, (int64_t)INT32_MAX));
-  const int tiles = (last - first + kTile - 1) / kTile;
+  const bool cut = split.seg != INT32_MAX;
+  // a sequence's last segment has no end to hand on: in its place stands the
+  // sequence's start state, read from here by the second pass, which may be
+  // writing final states over the initial ones
+  const int tiles = MODE == kSsmEnds && last == end ? 0 : (last - first + kTile - 1) / kTile;
   // a pair of channels is 16 bytes; the order of a row's pairs is turned so
   // that 8 helper lanes writing one each never meet on a bank
   auto slot = [](int t, int c) {
@@ -141,9 +147,11 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       bias[j] = a.bias && c < blk.n ? a.bias[blk.c0 + c] : 0.f;
       skip[j] = a.skip && c < blk.n ? a.skip[blk.c0 + c] : 0.f;
     }
-    Held<IO, E, VEC> ru, rd, rz, ro;
-    Held<IO, BN, true> rb, rc;   // bc_vec, and fp32 either way
-    Held<IO, BN, false> sb, sc;  // bf16 otherwise
+    struct Set {  // a tile's values on their way
+      Held<IO, E, VEC> u, d, z, o;
+      Held<IO, BN, true> b, c;     // bc_vec, and fp32 either way
+      Held<IO, BN, false> b1, c1;  // bf16 otherwise
+    } set;
     constexpr bool ONE = sizeof(IO) == 4;
     auto load_e = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, E, VEC>& r) {
       r.clear();
@@ -151,10 +159,11 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         if (tok_of(0) < m && ch_of(0) < blk.n)
           r.all(p + (t0 + tok_of(0)) * stride + ch_of(0));
       } else {
+        const IO* q = p + (t0 + tok_of(0)) * stride + ch_of(0);
+        const int left = ch_of(0) < blk.n ? m - tok_of(0) : 0;
 #pragma unroll
         for (int j = 0; j < E; ++j)
-          if (tok_of(j) < m && ch_of(j) < blk.n)
-            r.one(j, p + (t0 + tok_of(j)) * stride + ch_of(j));
+          if (j * TSTEP < left) r.one(j, q + j * (TSTEP * stride));
       }
     };
     auto load_bc = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, BN, true>& r,
@@ -178,26 +187,26 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           }
       }
     };
-    auto load = [&](int i) {
+    auto load = [&](int i, Set& r) {
       const int t0 = first + i * kTile, m = min(kTile, last - t0);
-      load_e(delta, a.delta_stride, t0, m, rd);
-      load_e(u, a.u_stride, t0, m, ru);
-      load_bc(B, a.b_stride, t0, m, rb, sb);
+      load_e(delta, a.delta_stride, t0, m, r.d);
+      load_e(u, a.u_stride, t0, m, r.u);
+      load_bc(B, a.b_stride, t0, m, r.b, r.b1);
       if (WANT_Y) {
-        load_bc(C, a.c_stride, t0, m, rc, sc);
-        if (z) load_e(z, a.z_stride, t0, m, rz);
+        load_bc(C, a.c_stride, t0, m, r.c, r.c1);
+        if (z) load_e(z, a.z_stride, t0, m, r.z);
       }
-      if (MODE == kSsmSaveDz) load_e(dout, a.D, t0, m, ro);
+      if (MODE == kSsmSaveDz) load_e(dout, a.D, t0, m, r.o);
     };
     // what turns y into the result: (y + add) * mul, of the tile being
     // converted and of the one before
     float add[2][E], mul[2][E];
-    auto convert = [&](int i, float (&add_)[E], float (&mul_)[E]) {
+    auto convert = [&](int i, const Set& r, float (&add_)[E], float (&mul_)[E]) {
       const int t0 = first + i * kTile, m = min(kTile, last - t0), w = i & 1;
       float dt[E], dtu[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float raw = rd.get(j) + bias[VEC ? j : 0], uu = ru.get(j);
+        const float raw = r.d.get(j) + bias[VEC ? j : 0], uu = r.u.get(j);
         const bool real = tok_of(j) < m && ch_of(j) < blk.n;
         dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
         dtu[j] = dt[j] * uu;
@@ -205,8 +214,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           add_[j] = skip[VEC ? j : 0] * uu;
           float k = 1.f;
           if (z) {
-            const float g = rz.get(j), s = sigmoid_f(g);
-            k = MODE == kSsmOut ? g * s : ro.get(j) * silu_grad(g, s);
+            const float g = r.z.get(j), s = sigmoid_f(g);
+            k = MODE == kSsmOut ? g * s : r.o.get(j) * silu_grad(g, s);
           }
           mul_[j] = k;
         }
@@ -223,8 +232,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       }
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        s_b[w][bt][bn + j] = ONE || bc_vec ? rb.get(j) : sb.get(j);
-        if (WANT_Y) s_c[w][bt][bn + j] = ONE || bc_vec ? rc.get(j) : sc.get(j);
+        s_b[w][bt][bn + j] = ONE || bc_vec ? r.b.get(j) : r.b1.get(j);
+        if (WANT_Y) s_c[w][bt][bn + j] = ONE || bc_vec ? r.c.get(j) : r.c1.get(j);
       }
     };
     auto finish = [&](int i, const float (&add_)[E], const float (&mul_)[E]) {
@@ -238,18 +247,19 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           store_vec<IO, E>(out + (int64_t)(t0 + t) * a.D + c, r);
         }
       } else {
+        const int c = ch_of(0), left = c < blk.n ? m - tok_of(0) : 0;
+        IO* q = out + (int64_t)(t0 + tok_of(0)) * a.D + c;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int t = tok_of(j), c = ch_of(j);
-          if (t < m && c < blk.n)
-            out[(int64_t)(t0 + t) * a.D + c] = from_f32<IO>((s_y[w][t][c] + add_[j]) * mul_[j]);
-        }
+        for (int j = 0; j < E; ++j)
+          if (j * TSTEP < left)
+            q[j * (TSTEP * (int64_t)a.D)] =
+                from_f32<IO>((s_y[w][tok_of(j)][c] + add_[j]) * mul_[j]);
       }
     };
     if (tiles > 0) {
-      load(0);
-      convert(0, add[0], mul[0]);
-      if (tiles > 1) load(1);
+      load(0, set);
+      convert(0, set, add[0], mul[0]);
+      if (tiles > 1) load(1, set);
     }
     __syncthreads();
     for (int i = 0; i < tiles; i += 2) {
@@ -258,8 +268,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         if (i + k >= tiles) break;
         if (WANT_Y && i + k > 0) finish(i + k - 1, add[1 - k], mul[1 - k]);
         if (i + k + 1 < tiles) {
-          convert(i + k + 1, add[1 - k], mul[1 - k]);
-          if (i + k + 2 < tiles) load(i + k + 2);
+          convert(i + k + 1, set, add[1 - k], mul[1 - k]);
+          if (i + k + 2 < tiles) load(i + k + 2, set);
         }
         __syncthreads();
       }
@@ -285,9 +295,14 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   for (int i = 0; i < kSsmStates; ++i) {
     const bool real = on && n0 + i < a.S;
     A2[i] = real ? a.A[(int64_t)d * a.S + n0 + i] * kLog2e : 0.f;
-    h[i] = real && a.h0 && MODE != kSsmEnds ? a.h0[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
+    h[i] = real && a.h0 && (!cut || (MODE == kSsmEnds && last == end))
+               ? a.h0[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
   }
-  if (MODE != kSsmEnds) {  // the ends of the segments before this one
+  if (cut && MODE != kSsmEnds) {  // the start state and the segments before this one
+    const int64_t n = max((int64_t)1, ((int64_t)(end - start) + split.seg - 1) / split.seg);
+#pragma unroll
+    for (int i = 0; i < kSsmStates; ++i)
+      if (n0 + i < a.S) h[i] = split.ends[((id - piece + n - 1) * a.D + d) * a.S + n0 + i];
     for (int k = 0; k < piece; ++k) {
       const int64_t row = (id - piece + k) * a.D + d;
       const float sum = split.steps[row];
@@ -524,9 +539,30 @@ cudaError_t step_pick(const SsmArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Splitting costs a second pass over the recurrence (without its outputs), so
+// it pays where the sequences' own CTAs leave most of the SMs idle: a segment
+// is what each of the SMs' CTA slots (two an SM) would get of the whole, and
+// sequences are cut where they hold three of them.  One sequence of 4096 tokens
+// whole and split: 159 and 27 us with 256 channels, 161 and 122 us with 2048;
+// with 4096 channels, 2.3 segments, 198 and 230 us.  Packed lengths are not
+// known on the host; their longest is taken to be 2.5 times the mean.
+int ssm_segment(const SsmArgs& a, int sms) {
+  if (a.n_seqs < 1) return INT32_MAX;
+  const int64_t blocks = ssm_blocks(a, kSsmThreads / ssm_lanes(a.S)), slots = 2 * (int64_t)sms;
+  int64_t seg = (a.tokens * blocks + slots - 1) / slots;
+  seg = seg < kMinSegment ? kMinSegment : (seg + 31) / 32 * 32;
+  const double longest = (double)a.tokens / a.n_seqs * (a.cu && a.n_seqs > 1 ? 2.5 : 1.0);
+  return longest >= 3.0 * seg ? (int)seg : INT32_MAX;
+}
+
 size_t ssm_split_bytes(const SsmArgs& a, int seg) {
-  if (seg == INT32_MAX) return 0;
-  return (size_t)segments(a, seg) * a.D * (a.S + 1) * sizeof(float);
+  return seg == INT32_MAX ? 0 : (size_t)segments(a, seg) * a.D * (a.S + 1) * sizeof(float);
+}
+
+SsmSplit ssm_split_at(const SsmArgs& a, int seg, void* workspace) {
+  SsmSplit s{seg, static_cast<float*>(workspace), nullptr};
+  if (seg != INT32_MAX) s.steps = s.ends + segments(a, seg) * a.D * a.S;
+  return s;
 }
 
 namespace {
@@ -545,10 +581,14 @@ cudaError_t scan(const SsmArgs& a, const SsmSave* save, const SsmSplit& split, c
 }
 }  // namespace
 
-cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t st) {
+size_t ssm_fwd_workspace_bytes(const SsmArgs& a, int sms) {
+  return ssm_split_bytes(a, ssm_segment(a, sms));
+}
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, void* workspace, int sms, cudaStream_t st) {
   if (a.n_seqs == 0) return cudaSuccess;
-  const SsmSplit whole{INT32_MAX, nullptr, nullptr};
-  return a.bf16 ? scan<__nv_bfloat16>(a, nullptr, whole, st) : scan<float>(a, nullptr, whole, st);
+  const SsmSplit split = ssm_split_at(a, ssm_segment(a, sms), workspace);
+  return a.bf16 ? scan<__nv_bfloat16>(a, nullptr, split, st) : scan<float>(a, nullptr, split, st);
 }
 
 cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,

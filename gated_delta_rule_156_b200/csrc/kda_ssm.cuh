@@ -101,7 +101,8 @@ enum SsmMode {
 };
 // A split scan: segments of `seg` tokens; ends [segment id][D][S] their states
 // from zero, steps [segment id][D] their sums of steps (a segment's decay is
-// exp(A * sum of steps)).
+// exp(A * sum of steps)).  The row of a sequence's last segment holds the
+// sequence's start state.
 struct SsmSplit {
   int seg;  // INT32_MAX: not split
   float* ends;
@@ -112,7 +113,11 @@ struct SsmSave {
   const void* d_out;  // for dz
   void* dz;
 };
+// Tokens per segment of a scan over `a` on a device of `sms` SMs, INT32_MAX
+// where it is not split, and the workspace that a split takes.
+int ssm_segment(const SsmArgs& a, int sms);
 size_t ssm_split_bytes(const SsmArgs& a, int seg);
+SsmSplit ssm_split_at(const SsmArgs& a, int seg, void* workspace);
 cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
                             cudaStream_t stream);
 

@@ -126,13 +126,16 @@ typedef struct {
  *     y_t    = sum_n C_t[g, n] h_t[n] + skip[d] u_t
  *     out_t  = y_t silu(z_t)                        (y_t without z)
  *   u, delta, z : [B, T, D] io dtype, token strides; z may be NULL.
- *   A           : [D, S] fp32, used as given (negative for a decay).
+ *   A           : [D, S] fp32, finite, used as given (negative for a decay).
  *   Bm, Cm      : [B, T, G, S] io dtype, token and group strides.
  *   skip, delta_bias : [D] fp32, may be NULL.
  *   initial_state : [N, D, S] fp32, or NULL (zeros).
  *   out         : [B, T, D] io dtype, dense.
  *   final_state : [N, D, S] fp32 or NULL; may equal initial_state.
- * The state and all sums are fp32.
+ * The state and all sums are fp32.  Long sequences that would leave most of
+ * the SMs idle are scanned in segments side by side, which are then joined
+ * (exactly: the recurrence is linear in the state); that takes stream-ordered
+ * workspace of D (S + 1) floats a segment.
  */
 KDA_API kda_status kda_ssm_scan_fwd(
     const kda_ssm_shape* shape, const void* u, const void* delta,

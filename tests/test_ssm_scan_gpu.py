@@ -341,3 +341,28 @@ def test_refusals():
     with pytest.raises(K.KdaError):  # three groups of 16 channels
         x = torch.zeros(2, 10, 3, 16, dtype=torch.bfloat16, device=DEV)
         K.ssm_scan_fwd(d["u"], d["delta"], d["A"], x, x)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,D,S,G", [
+    ([700], 24, 16, 1),                   # one sequence in segments of 128
+    ([385], 9, 5, 3),                     # a last segment of one token
+    ([0, 1000, 3, 0, 128, 256, 1], 20, 16, 2),  # packed: ends on and off cuts
+    ([640], 6, 64, 1)])
+def test_split_into_segments(io, lens, D, S, G):
+    # few channels: the scan runs in segments side by side
+    offs = R.offsets_of(0, 0, lens)
+    cu = torch.tensor(offs, dtype=torch.int32, device=DEV) \
+        if len(lens) > 1 else None
+    d = make((1, offs[-1]), D, S, G, io, sum(lens) + D, past=len(lens))
+    compare(d, offs, cu)
+
+
+def test_split_in_place_and_repeated():
+    d = make((1, 2000), 64, 16, 1, "bf16", 31, past=1)
+    args = (d["u"], d["delta"], d["A"], d["Bm"], d["Cm"])
+    out, fin = K.ssm_scan_fwd(*args, initial_state=d["past"])
+    for _ in range(3):
+        st = d["past"].clone()
+        out2, _ = K.ssm_scan_fwd(*args, initial_state=st, final_state=st)
+        assert torch.equal(out, out2) and torch.equal(fin, st)
