@@ -5,10 +5,10 @@
 // initial state.  W is 2, 3 or 4, so an element costs 2 W flops and an
 // activation against 2 * sizeof(io) bytes: the kernels are bound by HBM.
 //
-// Work split: a thread owns VEC neighbouring channels (one 16-byte access a
-// token in the forward) and a run of consecutive tokens, over which the last
-// W - 1 inputs stay in registers.  The run's first W - 1 inputs are read by
-// the run before it as well; those reads come out of L2.
+// Work split: a thread owns VEC neighbouring channels and a run of consecutive
+// tokens, over which the last W - 1 inputs stay in registers.  The run's first
+// W - 1 inputs are read by the run before it as well; those reads come out of
+// L2.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -21,12 +21,24 @@ template <typename IO, int W, int VEC>
 struct Taps {
   float w[W][VEC], b[VEC];
   __device__ __forceinline__ void load(const ConvArgs& a, int c0) {
+    const float* p = a.weight + (size_t)c0 * W;
+    if (W == 4 && (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+      for (int i = 0; i < VEC; ++i) {  // a channel's taps are 16 bytes
+        const float4 v = reinterpret_cast<const float4*>(p)[i];
+        w[0][i] = v.x;
+        w[1][i] = v.y;
+        w[W > 2 ? 2 : 0][i] = v.z;
+        w[W - 1][i] = v.w;
+      }
+    } else {
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = a.weight[(size_t)(c0 + i) * W + j];
-      b[i] = a.bias ? a.bias[c0 + i] : 0.f;
+      for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = p[i * W + j];
     }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) b[i] = a.bias ? a.bias[c0 + i] : 0.f;
   }
 };
 
@@ -78,7 +90,7 @@ __device__ __forceinline__ void slide(float (&win)[W - 1][VEC], const float (&x)
 // Block (channel vectors, runs); the grid's runs go over all tokens, then
 // over the n_seqs * (W - 1) rows of the final states.
 template <typename IO, int W, int VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     conv_fwd_kernel(ConvArgs a, int nvec, int run, int64_t n_runs) {
   const int cv = blockIdx.y * blockDim.x + threadIdx.x;
   int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -111,23 +123,30 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       input_at<IO, W, VEC>(a, q, (int)t - (W - 1) + j, c0, win[j]);
-    for (; t < e; t += kUnroll) {
+    const IO* px = x + t * a.x_stride;
+    IO* po = out + t * a.D;
+    auto token = [&](const Raw<IO, VEC>& raw) {
+      float v[VEC], pre[VEC];
+      unpack(raw, v);
+      taps_dot<IO, W, VEC>(k, win, v, pre);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
+      store_vec<IO, VEC>(po, pre);
+      slide<W, VEC>(win, v);
+      po += a.D;
+    };
+    int left = (int)(e - t);
+    for (; left >= kUnroll; left -= kUnroll) {
       Raw<IO, VEC> raw[kUnroll];
-      const int m = (int)min((int64_t)kUnroll, e - t);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-        if (i < m) raw[i] = load_raw<IO, VEC>(x + (t + i) * a.x_stride);
+      for (int i = 0; i < kUnroll; ++i) raw[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+      px += kUnroll * a.x_stride;
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        if (i >= m) break;
-        float v[VEC], pre[VEC];
-        unpack(raw[i], v);
-        taps_dot<IO, W, VEC>(k, win, v, pre);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
-        store_vec<IO, VEC>(out + (t + i) * a.D, pre);
-        slide<W, VEC>(win, v);
-      }
+      for (int i = 0; i < kUnroll; ++i) token(raw[i]);
+    }
+    for (; left > 0; --left) {
+      token(load_raw<IO, VEC>(px));
+      px += a.x_stride;
     }
     t = e;
   }
@@ -139,7 +158,7 @@ __global__ void __launch_bounds__(256)
 // and db over the run itself.  The block's runs are summed in shared memory
 // in a fixed order; conv_weight_sum_kernel sums the blocks.  The rows of
 // d_initial_state are independent of the runs and have threads of their own.
-constexpr int kBwdLanes = 32, kBwdRuns = 8;
+constexpr int kBwdLanes = 32, kBwdRuns = 8, kBwdUnroll = 4;
 
 template <typename IO, int W, int VEC>
 __device__ void past_grad(const ConvArgs& a, const Taps<IO, W, VEC>& k, int64_t row,
@@ -219,42 +238,53 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
     }
-    for (int64_t u = t; u < stop; u += kUnroll) {
-      Raw<IO, VEC> rx[kUnroll], ry[kUnroll];
-      const int m = (int)min((int64_t)kUnroll, stop - u);
+    const IO* px = x + t * a.x_stride;
+    const IO* py = dy + t * a.D;
+    IO* po = dx + (t - (W - 1)) * a.D;
+    int skip = W - 1;  // places before the run, finished by others
+    auto token = [&](const Raw<IO, VEC>& rx, const Raw<IO, VEC>& ry, bool mine) {
+      float xv[VEC], dp[VEC], pre[VEC], done[VEC];
+      unpack(rx, xv);
+      unpack(ry, dp);
+      taps_dot<IO, W, VEC>(k, win, xv, pre);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-        if (i < m) {
-          rx[i] = load_raw<IO, VEC>(x + (u + i) * a.x_stride);
-          ry[i] = load_raw<IO, VEC>(dy + (u + i) * a.D);
+      for (int c = 0; c < VEC; ++c) {
+        dp[c] *= act_grad(pre[c], a.act);
+        if (mine) {
+          db[c] += dp[c];
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) dw[j][c] = fmaf(dp[c], win[j][c], dw[j][c]);
+          dw[W - 1][c] = fmaf(dp[c], xv[c], dw[W - 1][c]);
         }
+        done[c] = fmaf(k.w[0][c], dp[c], g[0][c]);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        if (i >= m) break;
-        const int64_t tau = u + i;
-        float xv[VEC], dp[VEC], pre[VEC], done[VEC];
-        unpack(rx[i], xv);
-        unpack(ry[i], dp);
-        taps_dot<IO, W, VEC>(k, win, xv, pre);
-        const bool mine = tau < e;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          dp[c] *= act_grad(pre[c], a.act);
-          if (mine) {
-            db[c] += dp[c];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) dw[j][c] = fmaf(dp[c], win[j][c], dw[j][c]);
-            dw[W - 1][c] = fmaf(dp[c], xv[c], dw[W - 1][c]);
-          }
-          done[c] = fmaf(k.w[0][c], dp[c], g[0][c]);
-#pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j) g[j][c] = fmaf(k.w[j + 1][c], dp[c], g[j + 1][c]);
-          g[W - 2][c] = k.w[W - 1][c] * dp[c];
-        }
-        const int64_t at = tau - (W - 1);
-        if (at >= t) store_vec<IO, VEC>(dx + at * a.D, done);
-        slide<W, VEC>(win, xv);
+        for (int j = 0; j + 1 < W - 1; ++j) g[j][c] = fmaf(k.w[j + 1][c], dp[c], g[j + 1][c]);
+        g[W - 2][c] = k.w[W - 1][c] * dp[c];
       }
+      if (skip > 0)
+        --skip;
+      else
+        store_vec<IO, VEC>(po, done);
+      po += a.D;
+      slide<W, VEC>(win, xv);
+    };
+    int left = (int)(e - t);
+    for (; left >= kBwdUnroll; left -= kBwdUnroll) {
+      Raw<IO, VEC> rx[kBwdUnroll], ry[kBwdUnroll];
+#pragma unroll
+      for (int i = 0; i < kBwdUnroll; ++i) {
+        rx[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+        ry[i] = load_raw<IO, VEC>(py + i * (int64_t)a.D);
+      }
+      px += kBwdUnroll * a.x_stride;
+      py += kBwdUnroll * (int64_t)a.D;
+#pragma unroll
+      for (int i = 0; i < kBwdUnroll; ++i) token(rx[i], ry[i], true);
+    }
+    for (int i = left + (int)(stop - e); i > 0; --i) {
+      token(load_raw<IO, VEC>(px), load_raw<IO, VEC>(py), left-- > 0);
+      px += a.x_stride;
+      py += a.D;
     }
     if (stop == q.end) {  // the sequence's last W - 1 places
 #pragma unroll
@@ -313,37 +343,49 @@ __global__ void conv_weight_sum_kernel(const float* __restrict__ part, int64_t n
   }
 }
 
-// One thread per (sequence, channel vector): T new tokens, state in place.
-template <typename IO, int W, int VEC>
+// T new tokens, state in place.  A thread owns VEC channels of NS sequences,
+// whose loads it issues together; the taps are read once for all of them.
+template <typename IO, int W, int VEC, int NS>
 __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a, int nvec) {
   const int cv = blockIdx.y * blockDim.x + threadIdx.x;
-  const int64_t n = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (cv >= nvec || n >= a.n_seqs) return;
+  const int64_t n0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * NS;
+  if (cv >= nvec || n0 >= a.n_seqs) return;
   const int c0 = cv * VEC;
-  IO* st = static_cast<IO*>(a.final_state) + n * (W - 1) * a.D + c0;
-  Raw<IO, VEC> keep[W - 1], rx;
+  const int64_t row = (int64_t)(W - 1) * a.D, xs = (int64_t)a.T * a.x_stride;
+  IO* st = static_cast<IO*>(a.final_state) + n0 * row + c0;
+  const IO* x = static_cast<const IO*>(a.x) + n0 * xs + c0;
+  IO* out = static_cast<IO*>(a.out) + n0 * a.T * a.D + c0;
+  Raw<IO, VEC> keep[NS][W - 1], rx[NS];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) keep[j] = load_raw<IO, VEC>(st + (int64_t)j * a.D);
-  const IO* x = static_cast<const IO*>(a.x) + n * a.T * a.x_stride + c0;
-  rx = load_raw<IO, VEC>(x);
-  Taps<IO, W, VEC> k;
-  k.load(a, c0);
-  float win[W - 1][VEC];
+  for (int k = 0; k < NS; ++k)
+    if (n0 + k < a.n_seqs) {
+      rx[k] = load_raw<IO, VEC>(x + k * xs);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) unpack(keep[j], win[j]);
-  IO* out = static_cast<IO*>(a.out) + n * a.T * a.D + c0;
-  for (int t = 0; t < a.T; ++t) {
-    float v[VEC], pre[VEC];
-    unpack(rx, v);
-    if (t + 1 < a.T) rx = load_raw<IO, VEC>(x + (int64_t)(t + 1) * a.x_stride);
-    taps_dot<IO, W, VEC>(k, win, v, pre);
+      for (int j = 0; j < W - 1; ++j)
+        keep[k][j] = load_raw<IO, VEC>(st + k * row + (int64_t)j * a.D);
+    }
+  Taps<IO, W, VEC> taps;
+  taps.load(a, c0);
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
-    store_vec<IO, VEC>(out + (int64_t)t * a.D, pre);
-    slide<W, VEC>(win, v);
+  for (int k = 0; k < NS; ++k) {
+    if (n0 + k >= a.n_seqs) return;
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) unpack(keep[k][j], win[j]);
+    for (int t = 0; t < a.T; ++t) {
+      float v[VEC], pre[VEC];
+      unpack(rx[k], v);
+      if (t + 1 < a.T) rx[k] = load_raw<IO, VEC>(x + k * xs + (int64_t)(t + 1) * a.x_stride);
+      taps_dot<IO, W, VEC>(taps, win, v, pre);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
+      store_vec<IO, VEC>(out + ((int64_t)k * a.T + t) * a.D, pre);
+      slide<W, VEC>(win, v);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      store_vec<IO, VEC>(st + k * row + (int64_t)j * a.D, win[j]);
   }
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_vec<IO, VEC>(st + (int64_t)j * a.D, win[j]);
 }
 
 // Channel lanes of a 256-thread block: the smallest power of two that covers
@@ -365,9 +407,9 @@ template <typename IO, int W, int VEC>
 cudaError_t fwd_launch(const ConvArgs& a, cudaStream_t stream) {
   const int nvec = a.D / VEC;
   const dim3 block = block_shape(nvec);
-  // 16 tokens a run re-read 3 of 19 inputs from L2; shorter runs when the
+  // 32 tokens a run re-read 3 of 35 inputs from L2; shorter runs when the
   // tokens would not give every SM its 2048 threads
-  int run = 16;
+  int run = 32;
   while (run > 4 && (a.tokens + run - 1) / run * nvec < (int64_t)148 * 2048) run /= 2;
   const int64_t n_runs = (a.tokens + run - 1) / run;
   const int64_t rows = n_runs + (a.final_state ? (int64_t)a.n_seqs * (W - 1) : 0);
@@ -380,8 +422,14 @@ template <typename IO, int W, int VEC>
 cudaError_t step_launch(const ConvArgs& a, cudaStream_t stream) {
   const int nvec = a.D / VEC;
   const dim3 block = block_shape(nvec);
-  const dim3 grid((a.n_seqs + block.y - 1) / block.y, (nvec + block.x - 1) / block.x);
-  conv_step_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec);
+  // four sequences a thread where that still fills the SMs
+  const int ns = (int64_t)a.n_seqs * nvec >= (int64_t)4 * 148 * 1024 ? 4 : 1;
+  const int64_t rows = (a.n_seqs + ns - 1) / ns;
+  const dim3 grid((unsigned)((rows + block.y - 1) / block.y), (nvec + block.x - 1) / block.x);
+  if (ns == 4)
+    conv_step_kernel<IO, W, VEC, 4><<<grid, block, 0, stream>>>(a, nvec);
+  else
+    conv_step_kernel<IO, W, VEC, 1><<<grid, block, 0, stream>>>(a, nvec);
   return cudaGetLastError();
 }
 
@@ -417,7 +465,7 @@ cudaError_t bwd_launch(const ConvArgs& a, float* part, cudaStream_t stream) {
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream) {
   if (a.bf16)
-    return vec_ok(a, 8, 16) ? KDA_CONV_W(fwd_launch, __nv_bfloat16, 8, a, stream)
+    return vec_ok(a, 4, 8) ? KDA_CONV_W(fwd_launch, __nv_bfloat16, 4, a, stream)
                             : KDA_CONV_W(fwd_launch, __nv_bfloat16, 1, a, stream);
   return vec_ok(a, 4, 16) ? KDA_CONV_W(fwd_launch, float, 4, a, stream)
                           : KDA_CONV_W(fwd_launch, float, 1, a, stream);
@@ -426,7 +474,7 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream) {
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t stream) {
   if (a.n_seqs == 0 || a.T == 0) return cudaSuccess;
   if (a.bf16)
-    return vec_ok(a, 8, 16) ? KDA_CONV_W(step_launch, __nv_bfloat16, 8, a, stream)
+    return vec_ok(a, 4, 8) ? KDA_CONV_W(step_launch, __nv_bfloat16, 4, a, stream)
                             : KDA_CONV_W(step_launch, __nv_bfloat16, 1, a, stream);
   return vec_ok(a, 4, 16) ? KDA_CONV_W(step_launch, float, 4, a, stream)
                           : KDA_CONV_W(step_launch, float, 1, a, stream);

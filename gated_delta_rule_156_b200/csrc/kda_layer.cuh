@@ -42,6 +42,12 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 1>& a, float (&v)[1]) {
   v[0] = __uint_as_float((uint32_t)a.r << 16);
 }
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 2>& a, float (&v)[2]) {
+  v[0] = bf_lo(a.r); v[1] = bf_hi(a.r);
+}
+__device__ __forceinline__ void unpack(const Raw<float, 2>& a, float (&v)[2]) {
+  v[0] = a.r.x; v[1] = a.r.y;
+}
 __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 4>& a, float (&v)[4]) {
   v[0] = bf_lo(a.r.x); v[1] = bf_hi(a.r.x); v[2] = bf_lo(a.r.y); v[3] = bf_hi(a.r.y);
 }
