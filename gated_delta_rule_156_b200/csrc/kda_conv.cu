@@ -17,81 +17,94 @@ namespace {
 
 constexpr int kUnroll = 4;  // token loads in flight per thread
 
+// A thread's channels go in pairs through the packed fp32 arithmetic.
 template <typename IO, int W, int VEC>
 struct Taps {
-  float w[W][VEC], b[VEC];
+  static constexpr int P = kPairs<VEC>;
+  f32x2 w[W][P], b[P];
   __device__ __forceinline__ void load(const ConvArgs& a, int c0) {
+    float t[2 * P][W];
     const float* p = a.weight + (size_t)c0 * W;
     if (W == 4 && (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {  // a channel's taps are 16 bytes
         const float4 v = reinterpret_cast<const float4*>(p)[i];
-        w[0][i] = v.x;
-        w[1][i] = v.y;
-        w[W > 2 ? 2 : 0][i] = v.z;
-        w[W - 1][i] = v.w;
+        t[i][0] = v.x;
+        t[i][1] = v.y;
+        t[i][2 % W] = v.z;
+        t[i][W - 1] = v.w;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = p[i * W + j];
+        for (int j = 0; j < W; ++j) t[i][j] = p[i * W + j];
     }
+    if (VEC == 1)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) b[i] = a.bias ? a.bias[c0 + i] : 0.f;
+      for (int j = 0; j < W; ++j) t[2 * P - 1][j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = pack2(t[2 * i][j], t[2 * i + 1][j]);
+      b[i] = a.bias ? pack2(a.bias[c0 + 2 * i], VEC > 1 ? a.bias[c0 + 2 * i + 1] : 0.f) : both(0.f);
+    }
   }
 };
 
 // Input at position t of a sequence (t >= start - (W-1)): x, or the past.
 template <typename IO, int W, int VEC>
-__device__ __forceinline__ void input_at(const ConvArgs& a, const SeqCursor& q, int t,
-                                         int c0, float (&v)[VEC]) {
+__device__ __forceinline__ void input_at(const ConvArgs& a, const SeqCursor& q, int t, int c0,
+                                         f32x2 (&v)[kPairs<VEC>]) {
   if (t >= q.start) {
-    load_vec<IO, VEC>(static_cast<const IO*>(a.x) + (int64_t)t * a.x_stride + c0, v);
+    load_pairs<IO, VEC>(static_cast<const IO*>(a.x) + (int64_t)t * a.x_stride + c0, v);
   } else if (a.past) {
     const int64_t row = (int64_t)q.s * (W - 1) + (t - q.start + W - 1);
-    load_vec<IO, VEC>(static_cast<const IO*>(a.past) + row * a.D + c0, v);
+    load_pairs<IO, VEC>(static_cast<const IO*>(a.past) + row * a.D + c0, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+    for (int i = 0; i < kPairs<VEC>; ++i) v[i] = both(0.f);
   }
 }
 
-__device__ __forceinline__ float act_f(float x, int act) {
-  return act == kActSilu ? x * sigmoid_f(x) : x;
+__device__ __forceinline__ f32x2 act2(f32x2 x, int act) {
+  return act == kActSilu ? mul2(x, sigmoid2(x)) : x;
 }
-__device__ __forceinline__ float act_grad(float x, int act) {
-  return act == kActSilu ? silu_grad(x, sigmoid_f(x)) : 1.f;
+// d act(x) / dx: s (1 + x (1 - s)) for SiLU
+__device__ __forceinline__ f32x2 act_grad2(f32x2 x, int act) {
+  if (act != kActSilu) return both(1.f);
+  const f32x2 s = sigmoid2(x);
+  return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f)));
 }
 
-template <typename IO, int W, int VEC>
-__device__ __forceinline__ void taps_dot(const Taps<IO, W, VEC>& k,
-                                         const float (&win)[W - 1][VEC],
-                                         const float (&x)[VEC], float (&pre)[VEC]) {
+template <typename IO, int W, int VEC, int P>
+__device__ __forceinline__ void taps_dot(const Taps<IO, W, VEC>& k, const f32x2 (&win)[W - 1][P],
+                                         const f32x2 (&x)[P], f32x2 (&pre)[P]) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float p = k.b[i];
+  for (int i = 0; i < P; ++i) {
+    f32x2 p = k.b[i];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][i], win[j][i], p);
-    pre[i] = fmaf(k.w[W - 1][i], x[i], p);
+    for (int j = 0; j < W - 1; ++j) p = fma2(k.w[j][i], win[j][i], p);
+    pre[i] = fma2(k.w[W - 1][i], x[i], p);
   }
 }
 
-template <int W, int VEC>
-__device__ __forceinline__ void slide(float (&win)[W - 1][VEC], const float (&x)[VEC]) {
+template <int W, int P>
+__device__ __forceinline__ void slide(f32x2 (&win)[W - 1][P], const f32x2 (&x)[P]) {
 #pragma unroll
   for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) win[j][i] = win[j + 1][i];
+    for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) win[W - 2][i] = x[i];
+  for (int i = 0; i < P; ++i) win[W - 2][i] = x[i];
 }
 
 // Block (channel vectors, runs); the grid's runs go over all tokens, then
 // over the n_seqs * (W - 1) rows of the final states.
 template <typename IO, int W, int VEC>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, 3)
     conv_fwd_kernel(ConvArgs a, int nvec, int run, int64_t n_runs) {
+  constexpr int P = kPairs<VEC>;
   const int cv = blockIdx.y * blockDim.x + threadIdx.x;
   int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (cv >= nvec) return;
@@ -102,9 +115,9 @@ __global__ void __launch_bounds__(256, 4)
     SeqCursor q;
     q.s = (int)(r / (W - 1));
     seq_range(a.cu, q.s, a.T, &q.start, &q.end);
-    float v[VEC];
+    f32x2 v[P];
     input_at<IO, W, VEC>(a, q, q.end - (W - 1) + (int)(r % (W - 1)), c0, v);
-    store_vec<IO, VEC>(static_cast<IO*>(a.final_state) + r * a.D + c0, v);
+    store_pairs<IO, VEC>(static_cast<IO*>(a.final_state) + r * a.D + c0, v);
     return;
   }
   Taps<IO, W, VEC> k;
@@ -119,30 +132,40 @@ __global__ void __launch_bounds__(256, 4)
     if (t < q.start) t = q.start;
     const int64_t e = min((int64_t)q.end, t1);
     if (t >= e) break;
-    float win[W - 1][VEC];
+    f32x2 win[W - 1][P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       input_at<IO, W, VEC>(a, q, (int)t - (W - 1) + j, c0, win[j]);
     const IO* px = x + t * a.x_stride;
     IO* po = out + t * a.D;
     auto token = [&](const Raw<IO, VEC>& raw) {
-      float v[VEC], pre[VEC];
-      unpack(raw, v);
+      f32x2 v[P], pre[P];
+      unpack_pairs<IO, VEC>(raw, v);
       taps_dot<IO, W, VEC>(k, win, v, pre);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
-      store_vec<IO, VEC>(po, pre);
-      slide<W, VEC>(win, v);
+      for (int i = 0; i < P; ++i) pre[i] = act2(pre[i], a.act);
+      store_pairs<IO, VEC>(po, pre);
+      slide<W>(win, v);
       po += a.D;
     };
+    // groups of tokens; the next group's loads go out before this one's work
     int left = (int)(e - t);
-    for (; left >= kUnroll; left -= kUnroll) {
-      Raw<IO, VEC> raw[kUnroll];
+    Raw<IO, VEC> raw[2][kUnroll];
+    auto fetch = [&](Raw<IO, VEC>(&r)[kUnroll]) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) raw[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+      for (int i = 0; i < kUnroll; ++i) r[i] = load_raw<IO, VEC>(px + i * a.x_stride);
       px += kUnroll * a.x_stride;
+    };
+    if (left >= kUnroll) fetch(raw[0]);
+    while (left >= kUnroll) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) token(raw[i]);
+      for (int h = 0; h < 2; ++h) {
+        if (left < kUnroll) break;
+        left -= kUnroll;
+        if (left >= kUnroll) fetch(raw[h ^ 1]);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) token(raw[h][i]);
+      }
     }
     for (; left > 0; --left) {
       token(load_raw<IO, VEC>(px));
@@ -168,37 +191,38 @@ __device__ void past_grad(const ConvArgs& a, const Taps<IO, W, VEC>& k, int64_t 
   const int r = (int)(row % (W - 1));
   seq_range(a.cu, q.s, a.T, &q.start, &q.end);
   const int len = q.end - q.start;
-  float g[VEC];
+  constexpr int P = kPairs<VEC>;
+  f32x2 g[P];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) g[i] = 0.f;
+  for (int i = 0; i < P; ++i) g[i] = both(0.f);
   // row r of the past is input r-(W-1); token tau <= r reads it with tap r-tau
   for (int tau = 0; tau <= r && tau < len; ++tau) {
-    float win[W - 1][VEC], x[VEC], pre[VEC], dy[VEC];
+    f32x2 win[W - 1][P], x[P], pre[P], dy[P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       input_at<IO, W, VEC>(a, q, q.start + tau - (W - 1) + j, c0, win[j]);
     input_at<IO, W, VEC>(a, q, q.start + tau, c0, x);
     taps_dot<IO, W, VEC>(k, win, x, pre);
-    load_vec<IO, VEC>(static_cast<const IO*>(a.d_out) + (int64_t)(q.start + tau) * a.D + c0,
-                      dy);
+    load_pairs<IO, VEC>(static_cast<const IO*>(a.d_out) + (int64_t)(q.start + tau) * a.D + c0,
+                        dy);
 #pragma unroll
     for (int j = 0; j < W; ++j)
       if (j == r - tau)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          g[i] = fmaf(k.w[j][i], dy[i] * act_grad(pre[i], a.act), g[i]);
+        for (int i = 0; i < P; ++i)
+          g[i] = fma2(k.w[j][i], mul2(dy[i], act_grad2(pre[i], a.act)), g[i]);
   }
   if (a.d_final && r >= len) {  // a short sequence keeps this row
-    float v[VEC];
-    load_vec<IO, VEC>(static_cast<const IO*>(a.d_final) + (row - len) * a.D + c0, v);
+    f32x2 v[P];
+    load_pairs<IO, VEC>(static_cast<const IO*>(a.d_final) + (row - len) * a.D + c0, v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) g[i] += v[i];
+    for (int i = 0; i < P; ++i) g[i] = add2(g[i], v[i]);
   }
-  store_vec<IO, VEC>(static_cast<IO*>(a.d_past) + row * a.D + c0, g);
+  store_pairs<IO, VEC>(static_cast<IO*>(a.d_past) + row * a.D + c0, g);
 }
 
 template <typename IO, int W, int VEC>
-__global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
+__global__ void __launch_bounds__(kBwdLanes* kBwdRuns, 2)
     conv_bwd_kernel(ConvArgs a, int nvec, int run, int64_t n_blocks,
                     float* __restrict__ part) {
   __shared__ float s_part[kBwdRuns][W + 1][kBwdLanes][VEC];
@@ -212,12 +236,13 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
     if (on && row < (int64_t)a.n_seqs * (W - 1)) past_grad<IO, W, VEC>(a, k, row, c0);
     return;
   }
-  float dw[W][VEC], db[VEC];
+  constexpr int P = kPairs<VEC>;
+  f32x2 dw[W][P], db[P];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    db[i] = 0.f;
+  for (int i = 0; i < P; ++i) {
+    db[i] = both(0.f);
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    for (int j = 0; j < W; ++j) dw[j][i] = both(0.f);
   }
   const IO* x = static_cast<const IO*>(a.x) + c0;
   const IO* dy = static_cast<const IO*>(a.d_out) + c0;
@@ -231,55 +256,65 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
     const int64_t e = min((int64_t)q.end, t1);
     if (t >= e) break;
     const int64_t stop = min((int64_t)q.end, e + W - 1);
-    float win[W - 1][VEC], g[W - 1][VEC];
+    f32x2 win[W - 1][P], g[W - 1][P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       input_at<IO, W, VEC>(a, q, (int)t - (W - 1) + j, c0, win[j]);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) g[j][i] = 0.f;
+      for (int i = 0; i < P; ++i) g[j][i] = both(0.f);
     }
     const IO* px = x + t * a.x_stride;
     const IO* py = dy + t * a.D;
     IO* po = dx + (t - (W - 1)) * a.D;
     int skip = W - 1;  // places before the run, finished by others
     auto token = [&](const Raw<IO, VEC>& rx, const Raw<IO, VEC>& ry, bool mine) {
-      float xv[VEC], dp[VEC], pre[VEC], done[VEC];
-      unpack(rx, xv);
-      unpack(ry, dp);
+      f32x2 xv[P], dp[P], pre[P], done[P];
+      unpack_pairs<IO, VEC>(rx, xv);
+      unpack_pairs<IO, VEC>(ry, dp);
       taps_dot<IO, W, VEC>(k, win, xv, pre);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        dp[c] *= act_grad(pre[c], a.act);
+      for (int c = 0; c < P; ++c) {
+        dp[c] = mul2(dp[c], act_grad2(pre[c], a.act));
         if (mine) {
-          db[c] += dp[c];
+          db[c] = add2(db[c], dp[c]);
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) dw[j][c] = fmaf(dp[c], win[j][c], dw[j][c]);
-          dw[W - 1][c] = fmaf(dp[c], xv[c], dw[W - 1][c]);
+          for (int j = 0; j < W - 1; ++j) dw[j][c] = fma2(dp[c], win[j][c], dw[j][c]);
+          dw[W - 1][c] = fma2(dp[c], xv[c], dw[W - 1][c]);
         }
-        done[c] = fmaf(k.w[0][c], dp[c], g[0][c]);
+        done[c] = fma2(k.w[0][c], dp[c], g[0][c]);
 #pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) g[j][c] = fmaf(k.w[j + 1][c], dp[c], g[j + 1][c]);
-        g[W - 2][c] = k.w[W - 1][c] * dp[c];
+        for (int j = 0; j + 1 < W - 1; ++j) g[j][c] = fma2(k.w[j + 1][c], dp[c], g[j + 1][c]);
+        g[W - 2][c] = mul2(k.w[W - 1][c], dp[c]);
       }
       if (skip > 0)
         --skip;
       else
-        store_vec<IO, VEC>(po, done);
+        store_pairs<IO, VEC>(po, done);
       po += a.D;
-      slide<W, VEC>(win, xv);
+      slide<W>(win, xv);
     };
+    // groups of tokens; the next group's loads go out before this one's work
     int left = (int)(e - t);
-    for (; left >= kBwdUnroll; left -= kBwdUnroll) {
-      Raw<IO, VEC> rx[kBwdUnroll], ry[kBwdUnroll];
+    Raw<IO, VEC> rx[2][kBwdUnroll], ry[2][kBwdUnroll];
+    auto fetch = [&](Raw<IO, VEC>(&qx)[kBwdUnroll], Raw<IO, VEC>(&qy)[kBwdUnroll]) {
 #pragma unroll
       for (int i = 0; i < kBwdUnroll; ++i) {
-        rx[i] = load_raw<IO, VEC>(px + i * a.x_stride);
-        ry[i] = load_raw<IO, VEC>(py + i * (int64_t)a.D);
+        qx[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+        qy[i] = load_raw<IO, VEC>(py + i * (int64_t)a.D);
       }
       px += kBwdUnroll * a.x_stride;
       py += kBwdUnroll * (int64_t)a.D;
+    };
+    if (left >= kBwdUnroll) fetch(rx[0], ry[0]);
+    while (left >= kBwdUnroll) {
 #pragma unroll
-      for (int i = 0; i < kBwdUnroll; ++i) token(rx[i], ry[i], true);
+      for (int h = 0; h < 2; ++h) {
+        if (left < kBwdUnroll) break;
+        left -= kBwdUnroll;
+        if (left >= kBwdUnroll) fetch(rx[h ^ 1], ry[h ^ 1]);
+#pragma unroll
+        for (int i = 0; i < kBwdUnroll; ++i) token(rx[h][i], ry[h][i], true);
+      }
     }
     for (int i = left + (int)(stop - e); i > 0; --i) {
       token(load_raw<IO, VEC>(px), load_raw<IO, VEC>(py), left-- > 0);
@@ -292,24 +327,27 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns)
         const int64_t at = stop - (W - 1) + j;
         if (at >= t && at < e) {
           if (a.d_final) {
-            float v[VEC];
-            load_vec<IO, VEC>(static_cast<const IO*>(a.d_final) +
-                                  ((int64_t)q.s * (W - 1) + j) * a.D + c0, v);
+            f32x2 v[P];
+            load_pairs<IO, VEC>(static_cast<const IO*>(a.d_final) +
+                                    ((int64_t)q.s * (W - 1) + j) * a.D + c0, v);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) g[j][i] += v[i];
+            for (int i = 0; i < P; ++i) g[j][i] = add2(g[j][i], v[i]);
           }
-          store_vec<IO, VEC>(dx + at * a.D, g[j]);
+          store_pairs<IO, VEC>(dx + at * a.D, g[j]);
         }
       }
     }
     t = e;
   }
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
+  for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int j = 0; j < W; ++j) s_part[threadIdx.y][j][threadIdx.x][i] = dw[j][i];
-    s_part[threadIdx.y][W][threadIdx.x][i] = db[i];
-  }
+    for (int i = 0; i < P; ++i) {
+      float lo, hi;
+      unpack2(j < W ? dw[j % W][i] : db[i], lo, hi);
+      s_part[threadIdx.y][j][threadIdx.x][2 * i] = lo;
+      if (VEC > 1) s_part[threadIdx.y][j][threadIdx.x][(2 * i + 1) % VEC] = hi;
+    }
   __syncthreads();
   // part[block][tap or bias][channel]
   const int tid = threadIdx.y * kBwdLanes + threadIdx.x;
@@ -350,6 +388,7 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a, int nvec) {
   const int cv = blockIdx.y * blockDim.x + threadIdx.x;
   const int64_t n0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * NS;
   if (cv >= nvec || n0 >= a.n_seqs) return;
+  constexpr int P = kPairs<VEC>;
   const int c0 = cv * VEC;
   const int64_t row = (int64_t)(W - 1) * a.D, xs = (int64_t)a.T * a.x_stride;
   IO* st = static_cast<IO*>(a.final_state) + n0 * row + c0;
@@ -369,22 +408,22 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a, int nvec) {
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     if (n0 + k >= a.n_seqs) return;
-    float win[W - 1][VEC];
+    f32x2 win[W - 1][P];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) unpack(keep[k][j], win[j]);
+    for (int j = 0; j < W - 1; ++j) unpack_pairs<IO, VEC>(keep[k][j], win[j]);
     for (int t = 0; t < a.T; ++t) {
-      float v[VEC], pre[VEC];
-      unpack(rx[k], v);
+      f32x2 v[P], pre[P];
+      unpack_pairs<IO, VEC>(rx[k], v);
       if (t + 1 < a.T) rx[k] = load_raw<IO, VEC>(x + k * xs + (int64_t)(t + 1) * a.x_stride);
       taps_dot<IO, W, VEC>(taps, win, v, pre);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) pre[c] = act_f(pre[c], a.act);
-      store_vec<IO, VEC>(out + ((int64_t)k * a.T + t) * a.D, pre);
-      slide<W, VEC>(win, v);
+      for (int c = 0; c < P; ++c) pre[c] = act2(pre[c], a.act);
+      store_pairs<IO, VEC>(out + ((int64_t)k * a.T + t) * a.D, pre);
+      slide<W>(win, v);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      store_vec<IO, VEC>(st + k * row + (int64_t)j * a.D, win[j]);
+      store_pairs<IO, VEC>(st + k * row + (int64_t)j * a.D, win[j]);
   }
 }
 

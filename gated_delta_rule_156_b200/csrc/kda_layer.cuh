@@ -163,6 +163,46 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+  float a, b;
+  unpack2(mul2(x, both(-kLog2e)), a, b);
+  unpack2(add2(pack2(ex2_f(a), ex2_f(b)), both(1.f)), a, b);
+  return pack2(rcp_f(a), rcp_f(b));
+}
+
+// VEC elements as pairs; a single one is a pair with 0.
+template <int VEC>
+constexpr int kPairs = (VEC + 1) / 2;
+template <typename IO, int VEC>
+__device__ __forceinline__ void unpack_pairs(const Raw<IO, VEC>& a, f32x2 (&p)[kPairs<VEC>]) {
+  float v[VEC];
+  unpack(a, v);
+#pragma unroll
+  for (int i = 0; i < kPairs<VEC>; ++i) p[i] = pack2(v[2 * i], 2 * i + 1 < VEC ? v[(2 * i + 1) % VEC] : 0.f);
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void load_pairs(const IO* q, f32x2 (&p)[kPairs<VEC>]) {
+  unpack_pairs<IO, VEC>(load_raw<IO, VEC>(q), p);
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void store_pairs(IO* q, const f32x2 (&p)[kPairs<VEC>]) {
+  float v[VEC];
+#pragma unroll
+  for (int i = 0; i < kPairs<VEC>; ++i) {
+    float lo, hi;
+    unpack2(p[i], lo, hi);
+    v[2 * i] = lo;
+    if (2 * i + 1 < VEC) v[(2 * i + 1) % VEC] = hi;
+  }
+  store_vec<IO, VEC>(q, v);
+}
+
 // The sequence that owns a token of the flat token axis.
 struct SeqCursor {
   int s, start, end;  // token range [start, end) of sequence s
