@@ -8,108 +8,151 @@
 // dw = sum over rows of dy vhat, with vhat = v r.
 //
 // A row is read once and its elements stay in registers across both norms, so
-// the kernels are bound by HBM.  Work split: TPR threads own a row (part of a
-// warp for a head's row, a whole block for a wide one) and each of them the
-// same elements of every row it meets, so weights are loaded once and the
-// weights' gradients are register sums; the grid is the resident blocks only.
+// HBM is the bound; to reach it, a row's fixed cost (its sums over threads, its
+// addresses) must be spread over many elements a thread.  Work split: TPR
+// threads own a row (part of a warp for a head's row, a block for a wide one)
+// with up to 32 elements a thread forward, 16 backward, and several blocks an
+// SM, so that one row's loads run under another's sums.  (With 8 elements a
+// thread and one or two blocks an SM, rows prefetched through registers or an
+// asynchronous ring included, 16384 x 4096 took 0.21 to 0.33 ms.)  Each thread
+// meets the same elements of every row, so the weights' gradients are sums of
+// its own, kept in shared memory backward; the weights come out of L1, where
+// the rows do not stay.  The grid is the resident blocks only.
 #include "kda_layer.cuh"
 
 namespace kda {
 
 namespace {
 
-struct Act2 {
-  float f, d;  // act(g) and its derivative
+struct Gate {
+  bool none, silu;
+  // act(g) of a pair
+  __device__ __forceinline__ f32x2 f(f32x2 g) const {
+    if (none) return g;
+    const f32x2 s = sigmoid2(g);
+    return silu ? mul2(s, g) : s;
+  }
+  // s: sigmoid(g) -> act(g) and act'(g) = s (k + m (1 - s)) with act = s m:
+  // m = 1, k = 0 for the sigmoid, m = g, k = 1 for SiLU
+  __device__ __forceinline__ void fd(f32x2 g, f32x2 s, f32x2& f_, f32x2& d_) const {
+    if (none) {
+      f_ = g;
+      d_ = both(1.f);
+      return;
+    }
+    const f32x2 t = fma2(s, both(-1.f), both(1.f));
+    f_ = silu ? mul2(s, g) : s;
+    d_ = mul2(s, silu ? fma2(g, t, both(1.f)) : t);
+  }
 };
-__device__ __forceinline__ float gate_f(float g, int act) {
-  if (act == kActNone) return g;
-  const float s = sigmoid_f(g);
-  return act == kActSilu ? g * s : s;
-}
-__device__ __forceinline__ Act2 gate_fd(float g, int act) {
-  if (act == kActNone) return Act2{g, 1.f};
-  const float s = sigmoid_f(g);
-  return act == kActSilu ? Act2{g * s, silu_grad(g, s)} : Act2{s, s * (1.f - s)};
+
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
 }
 
-// Sum of one value (or two) over the TPR threads of a row, in every one of them.  TPR <= 32:
-// shuffles.  Above, the row is the whole block: per-warp sums through shared
-// memory; `turn` alternates between two buffers, so that one barrier per sum
-// is enough (a buffer is written again only behind the next sum's barrier).
+// Sums of N <= 4 values over the TPR threads of a row, in every one of them.
+// TPR <= 32: exchanges.  Above, the row is the whole block: per-warp sums
+// through shared memory; `turn` alternates between two buffers, so that one
+// barrier per sum is enough (a buffer is written again only behind the next
+// sum's barrier).  Every warp adds the warps' values in the same order.
 struct RowSum {
   int tpr;
   int turn;
-  float2* buf;  // [2][32]
-  __device__ __forceinline__ float2 two(float a, float b) {
-    const int w = tpr < 32 ? tpr : 32;
-    for (int o = w >> 1; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (tpr <= 32) return make_float2(a, b);
-    float2* s = buf + turn * 32;
+  float4* buf;  // [2][16]
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (tpr > o)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (tpr <= 32) return;
+    float4* s = buf + turn * 16;
     turn ^= 1;
-    const int warps = tpr >> 5;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+    if ((threadIdx.x & 31) == 0)
+      s[threadIdx.x >> 5] = make_float4(v[0], v[1 % N], v[2 % N], v[3 % N]);
     __syncthreads();
-    // every warp sums the warps' values with the same tree
-    const int lane = threadIdx.x & 31;
-    float2 v = lane < warps ? s[lane] : make_float2(0.f, 0.f);
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    float4 t = s[0];
+    for (int i = 1; i < tpr >> 5; ++i) {
+      const float4 u = s[i];
+      t.x += u.x;
+      if (N > 1) t.y += u.y;
+      if (N > 2) t.z += u.z;
+      if (N > 3) t.w += u.w;
     }
-    return v;
+    v[0] = t.x;
+    if (N > 1) v[1 % N] = t.y;
+    if (N > 2) v[2 % N] = t.z;
+    if (N > 3) v[3 % N] = t.w;
   }
-  __device__ __forceinline__ float one(float a) { return two(a, 0.f).x; }
 };
 
 // Element offsets of a thread's vectors and the rows of its block.
 template <int VEC, int ITER>
 struct Place {
-  int lane, rows_per_block, sub;
-  int col[ITER];
-  bool on[ITER];
-  __device__ __forceinline__ Place(int tpr, int width) {
-    lane = threadIdx.x % tpr;
+  int rows_per_block, sub, col0, stride, width;
+  __device__ __forceinline__ Place(int tpr, int width_) {
     sub = threadIdx.x / tpr;
     rows_per_block = blockDim.x / tpr;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int c = (lane + i * tpr) * VEC;
-      on[i] = c < width;
-      col[i] = on[i] ? c : 0;
-    }
+    col0 = threadIdx.x % tpr * VEC;
+    stride = tpr * VEC;
+    width = width_;
   }
+  __device__ __forceinline__ int col(int i) const { return col0 + i * stride; }
+  __device__ __forceinline__ bool on(int i) const { return col(i) < width; }
 };
 
-template <int VEC, int ITER>
-__device__ __forceinline__ void load_weight(const float* w, const Place<VEC, ITER>& p,
-                                            float none, float (&v)[ITER][VEC]) {
+// A weight's values at a thread's columns, or 1 without the weight.  The
+// pointers may be 4-byte aligned only (then not `vec`).
+template <int VEC>
+__device__ __forceinline__ void weight_at(const float* w, bool vec, int col,
+                                          f32x2 (&v)[kPairs<VEC>]) {
+  if (!w) {
 #pragma unroll
-  for (int i = 0; i < ITER; ++i)
+    for (int i = 0; i < kPairs<VEC>; ++i) v[i] = both(1.f);
+  } else if (VEC >= 4 && vec) {
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) v[i][c] = w ? w[p.col[i] + c] : none;
-}
-
-template <typename IO, int VEC, int ITER>
-__device__ __forceinline__ void load_row(const IO* row, const Place<VEC, ITER>& p, bool row_on,
-                                         Raw<IO, VEC> (&v)[ITER]) {
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(w + col) + i);
+      v[2 * i % kPairs<VEC>] = pack2(t.x, t.y);
+      v[(2 * i + 1) % kPairs<VEC>] = pack2(t.z, t.w);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    if (row && row_on && p.on[i])
-      v[i] = load_raw<IO, VEC>(row + p.col[i]);
-    else
-      v[i] = Raw<IO, VEC>{};
+    for (int i = 0; i < kPairs<VEC>; ++i)
+      v[i] = pack2(__ldg(w + col + 2 * i), VEC > 1 ? __ldg(w + col + 2 * i + 1) : 0.f);
   }
 }
 
-template <typename IO, int VEC, int ITER>
-__device__ __forceinline__ void store_row(IO* row, const Place<VEC, ITER>& p, bool row_on,
-                                          const float (&v)[ITER][VEC]) {
+// A row's elements pass once: they do not stay in L1.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_once(const T* p) {
+  constexpr int BYTES = VEC * (int)sizeof(T);
+  Raw<T, VEC> r;
+  if constexpr (BYTES % 16 == 0) {
+    uint4* q = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-  for (int i = 0; i < ITER; ++i)
-    if (row_on && p.on[i]) store_vec<IO, VEC>(row + p.col[i], v[i]);
+    for (int i = 0; i < BYTES / 16; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                   : "l"(reinterpret_cast<const uint4*>(p) + i));
+  } else {
+    r = load_raw<T, VEC>(p);
+  }
+  return r;
+}
+
+// `row`: the row's first element, or null.
+template <typename T, int VEC, int ITER>
+__device__ __forceinline__ void load_row(const T* row, const Place<VEC, ITER>& p,
+                                         Raw<T, VEC> (&v)[ITER]) {
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    v[i] = Raw<T, VEC>{};
+    if (row && p.on(i)) v[i] = load_once<T, VEC>(row + p.col(i));
+  }
 }
 
 __device__ __forceinline__ int64_t strided(const NormArgs& a, int64_t row, int64_t stride) {
@@ -118,86 +161,137 @@ __device__ __forceinline__ int64_t strided(const NormArgs& a, int64_t row, int64
   return t * stride + (row - t * a.heads) * a.width;
 }
 
-template <typename IO, typename RT, int VEC, int ITER>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(NormArgs a, int tpr) {
-  __shared__ float2 s_sum[64];
+__device__ __forceinline__ bool aligned16(const void* a, const void* b, const void* c) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+           reinterpret_cast<uintptr_t>(c)) & 15) == 0;
+}
+
+// GATE: 0 none, 1 behind the norm, 2 before it.
+template <typename IO, typename RT, int VEC, int ITER, int GATE>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
+  constexpr int P = kPairs<VEC>;
+  __shared__ float4 s_sum[32];
   const Place<VEC, ITER> p(tpr, a.width);
   RowSum sum{tpr, 0, s_sum};
+  const Gate act{a.act == kActNone, a.act == kActSilu};
   const int64_t rows = a.tokens * a.heads;
   const float inv_w = 1.f / (float)a.width;
-  float wpost[ITER][VEC], scale[ITER][VEC], wpre[ITER][VEC];
-  load_weight(a.post_weight, p, 1.f, wpost);
-  load_weight(a.scale, p, 1.f, scale);
-  load_weight(a.pre_weight, p, 1.f, wpre);
+  const bool wvec = aligned16(a.post_weight, a.scale, a.pre_weight);
   const IO* x = static_cast<const IO*>(a.x);
   const IO* gate = static_cast<const IO*>(a.gate);
   const RT* res = static_cast<const RT*>(a.residual);
   for (int64_t base = (int64_t)blockIdx.x * p.rows_per_block; base < rows;
        base += (int64_t)gridDim.x * p.rows_per_block) {
-    const int64_t row = base + p.sub;
-    const bool on = row < rows;
-    Raw<IO, VEC> rx[ITER], rg[ITER];
+    const int64_t row = base + p.sub, at = row * a.width;
+    const bool row_on = row < rows;
+    Raw<IO, VEC> rx[ITER], rg[GATE ? ITER : 1];
     Raw<RT, VEC> rr[ITER];
-    load_row<IO>(x + (on ? strided(a, row, a.x_stride) : 0), p, on, rx);
-    load_row<IO>(gate ? gate + (on ? strided(a, row, a.gate_stride) : 0) : gate, p, on, rg);
-    load_row<RT>(res ? res + (on ? row : 0) * a.width : res, p, on, rr);
-    float h[ITER][VEC], act[ITER][VEC];
-    float ss = 0.f;
+    load_row<IO>(row_on ? x + strided(a, row, a.x_stride) : nullptr, p, rx);
+    if constexpr (GATE != 0)
+      load_row<IO>(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, p, rg);
+    load_row<RT>(row_on && res ? res + at : nullptr, p, rr);
+    f32x2 h[ITER][P];
+    float s[1];
+    f32x2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      unpack(rx[i], h[i]);
-      unpack(rg[i], act[i]);
+      unpack_pairs<IO, VEC>(rx[i], h[i]);
+      if constexpr (GATE == 2) {
+        f32x2 g[P];
+        unpack_pairs<IO, VEC>(rg[i], g);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        act[i][c] = gate ? gate_f(act[i][c], a.act) : 1.f;
-        if (a.gate_first) {
-          h[i][c] *= act[i][c];
-          act[i][c] = 1.f;
-        }
-        ss = fmaf(h[i][c], h[i][c], ss);
+        for (int c = 0; c < P; ++c) h[i][c] = mul2(h[i][c], act.f(g[c]));
       }
+#pragma unroll
+      for (int c = 0; c < P; ++c) acc = fma2(h[i][c], h[i][c], acc);
     }
     float r1 = 1.f;
-    if (a.post_weight) r1 = rsqrtf(sum.one(ss) * inv_w + a.eps);
-    ss = 0.f;
+    if (a.post_weight) {
+      s[0] = sum2(acc);
+      sum(s);
+      r1 = rsqrtf(s[0] * inv_w + a.eps);
+    }
+    acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      float v[VEC];
-      unpack(rr[i], v);
+      if (!p.on(i)) continue;
+      f32x2 w[P], sc[P], r[P];
+      weight_at<VEC>(a.post_weight, wvec, p.col(i), w);
+      weight_at<VEC>(a.scale, wvec, p.col(i), sc);
+      unpack_pairs<RT, VEC>(rr[i], r);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        const float q = h[i][c] * r1 * wpost[i][c] * act[i][c];
-        h[i][c] = fmaf(scale[i][c], q, v[c]);
-        if (p.on[i]) ss = fmaf(h[i][c], h[i][c], ss);
+      for (int c = 0; c < P; ++c) h[i][c] = mul2(mul2(h[i][c], both(r1)), w[c]);
+      if constexpr (GATE == 1) {
+        f32x2 g[P];
+        unpack_pairs<IO, VEC>(rg[i], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) h[i][c] = mul2(h[i][c], act.f(g[c]));
       }
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        h[i][c] = fma2(sc[c], h[i][c], r[c]);
+        acc = fma2(h[i][c], h[i][c], acc);
+      }
+      if (row_on) store_pairs<RT, VEC>(static_cast<RT*>(a.out) + at + p.col(i), h[i]);
     }
-    store_row<RT>(static_cast<RT*>(a.out) + (on ? row : 0) * a.width, p, on, h);
     if (a.pre_weight) {
-      const float r2 = rsqrtf(sum.one(ss) * inv_w + a.eps);
+      s[0] = sum2(acc);
+      sum(s);
+      const float r2 = rsqrtf(s[0] * inv_w + a.eps);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i)
+      for (int i = 0; i < ITER; ++i) {
+        if (!p.on(i)) continue;
+        f32x2 w[P];
+        weight_at<VEC>(a.pre_weight, wvec, p.col(i), w);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) h[i][c] *= r2 * wpre[i][c];
-      store_row<IO>(static_cast<IO*>(a.normed) + (on ? row : 0) * a.width, p, on, h);
+        for (int c = 0; c < P; ++c) h[i][c] = mul2(mul2(h[i][c], both(r2)), w[c]);
+        if (row_on) store_pairs<IO, VEC>(static_cast<IO*>(a.normed) + at + p.col(i), h[i]);
+      }
     }
   }
 }
 
+// s[0 .. VEC) += t u, a thread's own columns in shared memory
+template <int VEC>
+__device__ __forceinline__ void add_columns(float* s, const f32x2 (&t)[kPairs<VEC>],
+                                            const f32x2 (&u)[kPairs<VEC>]) {
+  if constexpr (VEC >= 4) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      ulonglong2* q = reinterpret_cast<ulonglong2*>(s) + i;
+      ulonglong2 v = *q;
+      v.x = fma2(t[2 * i], u[2 * i], v.x);
+      v.y = fma2(t[2 * i + 1], u[2 * i + 1], v.y);
+      *q = v;
+    }
+  } else {
+    s[0] += sum2(mul2(t[0], u[0]));  // the pair's other half is 0
+  }
+}
+
 // part[block * rows_per_block + sub][3][width]: the weights' gradients of one
-// thread's rows; norm_weight_sum_kernel sums them in a fixed order.
-template <typename IO, typename RT, int VEC, int ITER>
+// row place's rows; norm_weight_sum_kernel sums them in a fixed order.
+template <typename IO, typename RT, int VEC, int ITER, int GATE>
 __global__ void __launch_bounds__(512)
     norm_bwd_kernel(NormArgs a, int tpr, float* __restrict__ part) {
-  __shared__ float2 s_sum[64];
+  constexpr int P = kPairs<VEC>;
+  __shared__ float4 s_sum[32];
+  extern __shared__ __align__(16) float s_cols[];  // [rows of the block][3][padded width]
   const Place<VEC, ITER> p(tpr, a.width);
   RowSum sum{tpr, 0, s_sum};
+  const Gate act{a.act == kActNone, a.act == kActSilu};
   const int64_t rows = a.tokens * a.heads;
   const float inv_w = 1.f / (float)a.width;
-  float wpost[ITER][VEC], scale[ITER][VEC], wpre[ITER][VEC];
-  load_weight(a.post_weight, p, 1.f, wpost);
-  load_weight(a.scale, p, 1.f, scale);
-  load_weight(a.pre_weight, p, 1.f, wpre);
-  float dpost[ITER][VEC] = {}, dscale[ITER][VEC] = {}, dpre[ITER][VEC] = {};
+  const bool wvec = aligned16(a.post_weight, a.scale, a.pre_weight);
+  const int pitch = (a.width + 3) & ~3;
+  float* c_post = s_cols + p.sub * 3 * pitch;
+  float* c_scale = c_post + pitch;
+  float* c_pre = c_scale + pitch;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i)
+    if (p.on(i))
+      for (int c = 0; c < VEC; ++c)
+        c_post[p.col(i) + c] = c_scale[p.col(i) + c] = c_pre[p.col(i) + c] = 0.f;
   const IO* x = static_cast<const IO*>(a.x);
   const IO* gate = static_cast<const IO*>(a.gate);
   const RT* res = static_cast<const RT*>(a.residual);
@@ -206,129 +300,427 @@ __global__ void __launch_bounds__(512)
   const bool pre = a.pre_weight && dnorm;
   for (int64_t base = (int64_t)blockIdx.x * p.rows_per_block; base < rows;
        base += (int64_t)gridDim.x * p.rows_per_block) {
-    const int64_t row = base + p.sub;
-    const bool on = row < rows;
-    const int64_t at = (on ? row : 0) * a.width;
-    Raw<IO, VEC> rx[ITER], rg[ITER], rn[ITER];
+    const int64_t row = base + p.sub, at = row * a.width;
+    const bool row_on = row < rows;
+    Raw<IO, VEC> rx[ITER], rg[GATE ? ITER : 1], rn[ITER];
     Raw<RT, VEC> rr[ITER], ro[ITER];
-    load_row<IO>(x + (on ? strided(a, row, a.x_stride) : 0), p, on, rx);
-    load_row<IO>(gate ? gate + (on ? strided(a, row, a.gate_stride) : 0) : gate, p, on, rg);
-    load_row<RT>(res ? res + at : res, p, on, rr);
-    load_row<RT>(dout ? dout + at : dout, p, on, ro);
-    load_row<IO>(dnorm ? dnorm + at : dnorm, p, on, rn);
-    float r1 = 1.f, r2 = 0.f, ss = 0.f;
-    if (a.post_weight) {
+    load_row<IO>(row_on ? x + strided(a, row, a.x_stride) : nullptr, p, rx);
+    if constexpr (GATE != 0)
+      load_row<IO>(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, p, rg);
+    load_row<IO>(row_on && pre ? dnorm + at : nullptr, p, rn);
+    load_row<RT>(row_on && pre && res ? res + at : nullptr, p, rr);
+    load_row<RT>(row_on && dout ? dout + at : nullptr, p, ro);
+    // sg: sigmoid(gate); hat: x [act(gate)] r1; d: the gradient from out to x
+    f32x2 sg[GATE ? ITER : 1][P], out[ITER][P], d[ITER][P];
+    float r1 = 1.f;
+    auto h_of = [&](int i, f32x2(&h)[P]) {
+      unpack_pairs<IO, VEC>(rx[i], h);
+      if constexpr (GATE == 2) {
+        f32x2 g[P], f, fd;
+        unpack_pairs<IO, VEC>(rg[i], g);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        float v[VEC], g[VEC];
-        unpack(rx[i], v);
-        unpack(rg[i], g);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          if (gate && a.gate_first) v[c] *= gate_f(g[c], a.act);
-          ss = fmaf(v[c], v[c], ss);
+        for (int c = 0; c < P; ++c) {
+          act.fd(g[c], sg[i][c], f, fd);
+          h[c] = mul2(h[c], f);
         }
       }
-      r1 = rsqrtf(sum.one(ss) * inv_w + a.eps);
-      if (!on) r1 = 0.f;  // with eps 0 an absent row must not add 0 * inf
+    };
+    if constexpr (GATE != 0)
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        f32x2 g[P];
+        unpack_pairs<IO, VEC>(rg[i], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) sg[i][c] = act.none ? both(0.f) : sigmoid2(g[c]);
+      }
+    if (a.post_weight) {
+      f32x2 acc = both(0.f);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        f32x2 h[P];
+        h_of(i, h);
+#pragma unroll
+        for (int c = 0; c < P; ++c) acc = fma2(h[c], h[c], acc);
+      }
+      float s[1] = {sum2(acc)};
+      sum(s);
+      // with eps 0 an absent row must not add 0 * inf
+      r1 = row_on ? rsqrtf(s[0] * inv_w + a.eps) : 0.f;
     }
-    // hat: h r1; q: hat w_post (before a gate behind the norm); d: d out
-    float hat[ITER][VEC], d[ITER][VEC], q[ITER][VEC];
-    Act2 act[ITER][VEC];
-    float s1 = 0.f, s2 = 0.f;
+    float r2 = 0.f, m2 = 0.f;
+    if (pre) {
+      f32x2 acc1 = both(0.f), acc2 = both(0.f);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        if (!p.on(i)) continue;
+        f32x2 w[P], sc[P], wn[P], h[P], n[P], r[P];
+        weight_at<VEC>(a.post_weight, wvec, p.col(i), w);
+        weight_at<VEC>(a.scale, wvec, p.col(i), sc);
+        weight_at<VEC>(a.pre_weight, wvec, p.col(i), wn);
+        h_of(i, h);
+        unpack_pairs<IO, VEC>(rn[i], n);
+        unpack_pairs<RT, VEC>(rr[i], r);
+        f32x2 g[P];
+        if constexpr (GATE == 1) unpack_pairs<IO, VEC>(rg[i], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          f32x2 q = mul2(mul2(h[c], both(r1)), w[c]);
+          if constexpr (GATE == 1) {
+            f32x2 f, fd;
+            act.fd(g[c], sg[i][c], f, fd);
+            q = mul2(q, f);
+          }
+          out[i][c] = fma2(sc[c], q, r[c]);
+          acc1 = fma2(out[i][c], out[i][c], acc1);
+          acc2 = fma2(mul2(n[c], wn[c]), out[i][c], acc2);
+        }
+      }
+      float s[2] = {sum2(acc1), sum2(acc2)};
+      sum(s);
+      // d out += r2 (dn w - out r2 mean(dn w out r2))
+      r2 = row_on ? rsqrtf(s[0] * inv_w + a.eps) : 0.f;
+      m2 = -(s[1] * inv_w * r2 * r2);
+    }
+    f32x2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      float v[VEC], g[VEC], o[VEC], n[VEC], r[VEC];
-      unpack(rx[i], v);
-      unpack(rg[i], g);
-      unpack(rr[i], r);
-      unpack(ro[i], o);
-      unpack(rn[i], n);
+      if (!p.on(i)) continue;
+      const int col = p.col(i);
+      unpack_pairs<RT, VEC>(ro[i], d[i]);
+      if (pre) {
+        f32x2 wn[P], n[P], o2[P];
+        weight_at<VEC>(a.pre_weight, wvec, col, wn);
+        unpack_pairs<IO, VEC>(rn[i], n);
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        act[i][c] = gate ? gate_fd(g[c], a.act) : Act2{1.f, 0.f};
-        const float first = a.gate_first ? act[i][c].f : 1.f;
-        const float behind = a.gate_first ? 1.f : act[i][c].f;
-        hat[i][c] = v[c] * first * r1;
-        q[i][c] = hat[i][c] * wpost[i][c];
-        d[i][c] = o[c];
-        if (pre) {
-          const float out = fmaf(scale[i][c], q[i][c] * behind, r[c]);
-          if (p.on[i]) {
-            s1 = fmaf(out, out, s1);
-            s2 = fmaf(n[c] * wpre[i][c], out, s2);
-          }
+        for (int c = 0; c < P; ++c) {
+          d[i][c] = fma2(both(r2), fma2(out[i][c], both(m2), mul2(n[c], wn[c])), d[i][c]);
+          o2[c] = mul2(out[i][c], both(r2));
+        }
+        add_columns<VEC>(c_pre + col, n, o2);
+      }
+      if (a.dres && row_on) store_pairs<RT, VEC>(static_cast<RT*>(a.dres) + at + col, d[i]);
+      f32x2 w[P], sc[P], h[P], q[P], f[P], fd[P];
+      weight_at<VEC>(a.post_weight, wvec, col, w);
+      weight_at<VEC>(a.scale, wvec, col, sc);
+      h_of(i, h);
+      if constexpr (GATE == 1) {
+        f32x2 g[P];
+        unpack_pairs<IO, VEC>(rg[i], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) act.fd(g[c], sg[i][c], f[c], fd[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        h[c] = mul2(h[c], both(r1));
+        q[c] = mul2(h[c], w[c]);
+        if constexpr (GATE == 1) {
+          fd[c] = mul2(fd[c], q[c]);
+          q[c] = mul2(q[c], f[c]);
         }
       }
-    }
-    if (pre) {
-      const float2 t = sum.two(s1, s2);
-      r2 = on ? rsqrtf(t.x * inv_w + a.eps) : 0.f;
-      // d out += r2 (dn w - out r2 mean(dn w out r2))
-      const float m = t.y * inv_w * r2 * r2;
+      if (a.dscale) add_columns<VEC>(c_scale + col, d[i], q);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        float n[VEC], r[VEC];
-        unpack(rn[i], n);
-        unpack(rr[i], r);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const float behind = a.gate_first ? 1.f : act[i][c].f;
-          const float out = fmaf(scale[i][c], q[i][c] * behind, r[c]);
-          dpre[i][c] = fmaf(n[c], out * r2, dpre[i][c]);
-          d[i][c] = fmaf(r2, n[c] * wpre[i][c] - out * m, d[i][c]);
+      for (int c = 0; c < P; ++c) {
+        d[i][c] = mul2(d[i][c], sc[c]);
+        if constexpr (GATE == 1) {
+          fd[c] = mul2(fd[c], d[i][c]);
+          d[i][c] = mul2(d[i][c], f[c]);
         }
       }
-    }
-    if (a.dres) store_row<RT>(static_cast<RT*>(a.dres) + at, p, on, d);
-    float s3 = 0.f;
-    float dg[ITER][VEC];
+      if constexpr (GATE == 1)
+        if (row_on) store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + col, fd);
+      if (a.dpost) add_columns<VEC>(c_post + col, d[i], h);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        const float behind = a.gate_first ? 1.f : act[i][c].f;
-        dscale[i][c] = fmaf(d[i][c], q[i][c] * behind, dscale[i][c]);
-        const float dp = d[i][c] * scale[i][c];
-        dg[i][c] = dp * q[i][c] * act[i][c].d;  // the gate behind the norm
-        d[i][c] = dp * behind;                  // into q
-        dpost[i][c] = fmaf(d[i][c], hat[i][c], dpost[i][c]);
-        if (p.on[i]) s3 = fmaf(d[i][c] * wpost[i][c], hat[i][c], s3);
+      for (int c = 0; c < P; ++c) {
+        d[i][c] = mul2(d[i][c], w[c]);
+        acc = fma2(d[i][c], h[c], acc);
       }
+    }
+    float m1 = 0.f;
     if (a.post_weight) {
-      const float m = sum.one(s3) * inv_w;
-#pragma unroll
-      for (int i = 0; i < ITER; ++i)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-          d[i][c] = r1 * (d[i][c] * wpost[i][c] - hat[i][c] * m);
+      float s[1] = {sum2(acc)};
+      sum(s);
+      m1 = -(s[0] * inv_w * r1);  // hat = h r1
     }
-    if (a.gate_first) {  // d is the gradient of h = x act(g)
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        float v[VEC];
-        unpack(rx[i], v);
+    for (int i = 0; i < ITER; ++i) {
+      if (!p.on(i) || !row_on) continue;
+      const int col = p.col(i);
+      if (a.post_weight) {
+        f32x2 h[P];
+        h_of(i, h);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          dg[i][c] = d[i][c] * v[c] * act[i][c].d;
-          d[i][c] *= act[i][c].f;
-        }
+        for (int c = 0; c < P; ++c)
+          d[i][c] = mul2(both(r1), fma2(h[c], both(m1), d[i][c]));
       }
+      if constexpr (GATE == 2) {  // d is the gradient of h = x act(g)
+        f32x2 g[P], xv[P], dg[P];
+        unpack_pairs<IO, VEC>(rg[i], g);
+        unpack_pairs<IO, VEC>(rx[i], xv);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          f32x2 f, fd;
+          act.fd(g[c], sg[i][c], f, fd);
+          dg[c] = mul2(mul2(fd, xv[c]), d[i][c]);
+          d[i][c] = mul2(d[i][c], f);
+        }
+        store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + col, dg);
+      }
+      store_pairs<IO, VEC>(static_cast<IO*>(a.dx) + at + col, d[i]);
     }
-    if (gate) store_row<IO>(static_cast<IO*>(a.dgate) + at, p, on, dg);
-    store_row<IO>(static_cast<IO*>(a.dx) + at, p, on, d);
   }
-  const int64_t slot = (int64_t)blockIdx.x * p.rows_per_block + p.sub;
-  float* o = part + slot * 3 * a.width;
+  float* o = part + ((int64_t)blockIdx.x * p.rows_per_block + p.sub) * 3 * a.width;
 #pragma unroll
   for (int i = 0; i < ITER; ++i)
-    if (p.on[i])
-#pragma unroll
+    if (p.on(i))
       for (int c = 0; c < VEC; ++c) {
-        if (a.dpost) o[p.col[i] + c] = dpost[i][c];
-        if (a.dscale) o[a.width + p.col[i] + c] = dscale[i][c];
-        if (a.dpre) o[2 * a.width + p.col[i] + c] = dpre[i][c];
+        const int col = p.col(i) + c;
+        if (a.dpost) o[col] = c_post[col];
+        if (a.dscale) o[a.width + col] = c_scale[col];
+        if (a.dpre) o[2 * a.width + col] = c_pre[col];
       }
+}
+
+// The backward for wide rows (every thread VEC columns, no gaps): two rows at a
+// time, so that the weights' loads, the sums' barriers and the addresses serve
+// both.  The rows arrive through two slots of shared memory, filled by
+// asynchronous copies of 16 bytes: a thread copies just the elements that it
+// will read (no barrier), the next pair while it works on this one, and reads
+// them again wherever they are needed instead of holding them.  The weights
+// are in shared memory, their gradients in registers.
+constexpr int kPairRows = 2;
+
+template <typename T, int VEC>
+constexpr int kUnits = VEC * (int)sizeof(T) / 16;  // 16-byte units of a vector
+
+template <typename T, int VEC>
+__device__ __forceinline__ void send_vec(unsigned dst, int unit, const T* p) {
+#pragma unroll
+  for (int k = 0; k < kUnits<T, VEC>; ++k)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * unit),
+                 "l"(reinterpret_cast<const uint4*>(p) + k));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void take_vec(const unsigned char* s, int unit, bool on,
+                                         f32x2 (&v)[kPairs<VEC>]) {
+  Raw<T, VEC> raw{};
+  if (on) {
+    uint4* q = reinterpret_cast<uint4*>(&raw);
+#pragma unroll
+    for (int k = 0; k < kUnits<T, VEC>; ++k) q[k] = *reinterpret_cast<const uint4*>(s + k * unit);
+  }
+  unpack_pairs<T, VEC>(raw, v);
+}
+template <int VEC>
+__device__ __forceinline__ void shared_weight(const float* s, f32x2 (&v)[kPairs<VEC>]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    const ulonglong2 t = reinterpret_cast<const ulonglong2*>(s)[i];
+    v[2 * i] = t.x;
+    v[2 * i + 1] = t.y;
+  }
+}
+
+template <typename IO, typename RT, int VEC, int GATE, bool SILU>
+__global__ void __launch_bounds__(512)
+    norm_bwd_pair_kernel(NormArgs a, int slot_bytes, float* __restrict__ part) {
+  constexpr int P = kPairs<VEC>, R = kPairRows;
+  extern __shared__ __align__(16) unsigned char s_mem[];
+  __shared__ float4 s_sum[32];
+  RowSum sum{(int)blockDim.x, 0, s_sum};
+  const int col = threadIdx.x * VEC, unit = blockDim.x * 16;
+  const float inv_w = 1.f / (float)a.width;
+  float* s_post = reinterpret_cast<float*>(s_mem + 2 * slot_bytes);
+  float* s_scale = s_post + a.width;
+  float* s_pre = s_scale + a.width;
+  for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+    s_post[i] = a.post_weight ? a.post_weight[i] : 1.f;
+    s_scale[i] = a.scale ? a.scale[i] : 1.f;
+    s_pre[i] = a.pre_weight ? a.pre_weight[i] : 1.f;
+  }
+  const bool pre = a.pre_weight && a.d_normed, res = pre && a.residual, dout = a.d_out;
+  // units before each array in a slot's row
+  constexpr int UX = kUnits<IO, VEC>, UR = kUnits<RT, VEC>;
+  const int at_n = GATE ? 2 * UX : UX, at_r = at_n + (pre ? UX : 0), at_o = at_r + (res ? UR : 0),
+            row_units = at_o + (dout ? UR : 0);
+  const int64_t rows = a.tokens * a.heads, pairs = (rows + R - 1) / R;
+  unsigned char* mine = s_mem + threadIdx.x * 16;
+  const unsigned dst0 = (unsigned)__cvta_generic_to_shared(mine);
+  auto fetch = [&](int slot, int64_t pair) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = pair * R + j;
+      if (row < rows) {
+        const unsigned dst = dst0 + slot * slot_bytes + j * row_units * unit;
+        const int64_t at = row * a.width + col;
+        send_vec<IO, VEC>(dst, unit, static_cast<const IO*>(a.x) + strided(a, row, a.x_stride) + col);
+        if (GATE)
+          send_vec<IO, VEC>(dst + UX * unit, unit,
+                            static_cast<const IO*>(a.gate) + strided(a, row, a.gate_stride) + col);
+        if (pre) send_vec<IO, VEC>(dst + at_n * unit, unit, static_cast<const IO*>(a.d_normed) + at);
+        if (res) send_vec<RT, VEC>(dst + at_r * unit, unit, static_cast<const RT*>(a.residual) + at);
+        if (dout) send_vec<RT, VEC>(dst + at_o * unit, unit, static_cast<const RT*>(a.d_out) + at);
+      }
+    }
+    asm volatile("cp.async.commit_group;");
+  };
+  f32x2 dpost[P], dscale[P], dpre[P];
+#pragma unroll
+  for (int c = 0; c < P; ++c) dpost[c] = dscale[c] = dpre[c] = both(0.f);
+  int slot = 0;
+  if (blockIdx.x < pairs) fetch(0, blockIdx.x);
+  __syncthreads();
+  for (int64_t pair = blockIdx.x; pair < pairs; pair += gridDim.x, slot ^= 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // the other slot's last reads lie behind the last pair's barriers
+    if (pair + gridDim.x < pairs) fetch(slot ^ 1, pair + gridDim.x);
+    const int64_t at = pair * R * a.width + col;
+    const unsigned char* from = mine + slot * slot_bytes;
+    bool on[R];
+    const unsigned char* src[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      on[j] = pair * R + j < rows;
+      src[j] = from + j * row_units * unit;
+    }
+    // hat: x [act(gate)] r1; sg: sigmoid(gate); d: the gradient from out to x
+    f32x2 hat[R][P], sg[GATE ? R : 1][P], out[R][P];
+    float r1[R], r2[R], m[R], s2[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      f32x2 acc = both(0.f);
+      take_vec<IO, VEC>(src[j], unit, on[j], hat[j]);
+      if constexpr (GATE != 0) {
+        f32x2 g[P];
+        take_vec<IO, VEC>(src[j] + UX * unit, unit, on[j], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          sg[j][c] = sigmoid2(g[c]);
+          if (GATE == 2) hat[j][c] = mul2(hat[j][c], SILU ? mul2(sg[j][c], g[c]) : sg[j][c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < P; ++c) acc = fma2(hat[j][c], hat[j][c], acc);
+      s2[j] = sum2(acc);
+      r1[j] = 1.f;
+    }
+    if (a.post_weight) {
+      sum(s2);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        // with eps 0 an absent row must not add 0 * inf
+        r1[j] = on[j] ? rsqrtf(s2[j] * inv_w + a.eps) : 0.f;
+#pragma unroll
+        for (int c = 0; c < P; ++c) hat[j][c] = mul2(hat[j][c], both(r1[j]));
+      }
+    }
+    f32x2 w[P], sc[P];
+    shared_weight<VEC>(s_post + col, w);
+    shared_weight<VEC>(s_scale + col, sc);
+    if (pre) {
+      f32x2 wn[P];
+      shared_weight<VEC>(s_pre + col, wn);
+      float s4[2 * R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        f32x2 n[P], acc1 = both(0.f), acc2 = both(0.f);
+        take_vec<IO, VEC>(src[j] + at_n * unit, unit, on[j], n);
+        take_vec<RT, VEC>(src[j] + at_r * unit, unit, on[j] && res, out[j]);
+        f32x2 g[P];
+        if constexpr (GATE == 1 && SILU) take_vec<IO, VEC>(src[j] + UX * unit, unit, on[j], g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          f32x2 q = mul2(hat[j][c], w[c]);
+          if constexpr (GATE == 1) q = mul2(q, SILU ? mul2(sg[j][c], g[c]) : sg[j][c]);
+          out[j][c] = fma2(sc[c], q, out[j][c]);
+          acc1 = fma2(out[j][c], out[j][c], acc1);
+          acc2 = fma2(mul2(n[c], wn[c]), out[j][c], acc2);
+        }
+        s4[2 * j] = sum2(acc1);
+        s4[2 * j + 1] = sum2(acc2);
+      }
+      sum(s4);
+      // d out += r2 (dn w - out r2 mean(dn w out r2))
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        r2[j] = on[j] ? rsqrtf(s4[2 * j] * inv_w + a.eps) : 0.f;
+        m[j] = -(s4[2 * j + 1] * inv_w * r2[j] * r2[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      f32x2 d[P], acc = both(0.f);
+      take_vec<RT, VEC>(src[j] + at_o * unit, unit, on[j] && dout, d);
+      if (pre) {
+        f32x2 n[P], wn[P];
+        take_vec<IO, VEC>(src[j] + at_n * unit, unit, on[j], n);
+        shared_weight<VEC>(s_pre + col, wn);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          d[c] = fma2(both(r2[j]), fma2(out[j][c], both(m[j]), mul2(n[c], wn[c])), d[c]);
+          dpre[c] = fma2(n[c], mul2(out[j][c], both(r2[j])), dpre[c]);
+        }
+      }
+      if (a.dres && on[j]) store_pairs<RT, VEC>(static_cast<RT*>(a.dres) + at + j * a.width, d);
+      f32x2 g[P], dg[P];
+      if constexpr (GATE == 1 && SILU) take_vec<IO, VEC>(src[j] + UX * unit, unit, on[j], g);
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        f32x2 q = mul2(hat[j][c], w[c]);
+        if constexpr (GATE == 1) {
+          const f32x2 s = sg[j][c], t = fma2(s, both(-1.f), both(1.f));
+          const f32x2 f = SILU ? mul2(s, g[c]) : s;
+          dg[c] = mul2(mul2(s, SILU ? fma2(g[c], t, both(1.f)) : t), q);  // act'(g) q
+          q = mul2(q, f);
+          dscale[c] = fma2(d[c], q, dscale[c]);
+          d[c] = mul2(d[c], sc[c]);
+          dg[c] = mul2(dg[c], d[c]);
+          d[c] = mul2(d[c], f);
+        } else {
+          dscale[c] = fma2(d[c], q, dscale[c]);
+          d[c] = mul2(d[c], sc[c]);
+        }
+        dpost[c] = fma2(d[c], hat[j][c], dpost[c]);
+        d[c] = mul2(d[c], w[c]);
+        acc = fma2(d[c], hat[j][c], acc);
+        out[j][c] = d[c];
+      }
+      if constexpr (GATE == 1)
+        if (on[j]) store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + j * a.width, dg);
+      s2[j] = sum2(acc);
+    }
+    if (a.post_weight) sum(s2);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (!on[j]) continue;
+      f32x2 (&d)[P] = out[j];
+      if (a.post_weight) {
+        const float mean = -(s2[j] * inv_w);
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+          d[c] = mul2(both(r1[j]), fma2(hat[j][c], both(mean), d[c]));
+      }
+      if constexpr (GATE == 2) {  // d is the gradient of h = x act(g)
+        f32x2 g[P], xv[P], dg[P];
+        take_vec<IO, VEC>(src[j], unit, true, xv);
+        take_vec<IO, VEC>(src[j] + UX * unit, unit, true, g);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          const f32x2 s = sg[j][c], t = fma2(s, both(-1.f), both(1.f));
+          dg[c] = mul2(mul2(mul2(s, SILU ? fma2(g[c], t, both(1.f)) : t), xv[c]), d[c]);
+          d[c] = mul2(d[c], SILU ? mul2(s, g[c]) : s);
+        }
+        store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + j * a.width, dg);
+      }
+      store_pairs<IO, VEC>(static_cast<IO*>(a.dx) + at + j * a.width, d);
+    }
+    // without a sum nothing else separates this slot's reads from its refill,
+    // but they are this thread's own
+  }
+  float* o = part + (int64_t)blockIdx.x * 3 * a.width + col;
+  if (a.dpost) store_pairs<float, VEC>(o, dpost);
+  if (a.dscale) store_pairs<float, VEC>(o + a.width, dscale);
+  if (a.dpre) store_pairs<float, VEC>(o + 2 * a.width, dpre);
 }
 
 __global__ void norm_weight_sum_kernel(const float* __restrict__ part, int slots, int width,
@@ -349,28 +741,37 @@ __global__ void norm_weight_sum_kernel(const float* __restrict__ part, int slots
   }
 }
 
-// Threads per row and vectors per thread.  Up to 32 vectors a row is part of
-// a warp (the block holds several rows); above, the block is one row.
+// Threads per row and vectors per thread.  Up to 32 threads a row is part of a
+// warp (the block holds several rows); above, the block is one row.
 struct Shape {
   int tpr, block, iter;
 };
-Shape row_shape(int width, int vec, const int* iters, int n_iter, int max_tpr) {
-  const int nvec = (width + vec - 1) / vec;
-  Shape s{8, 0, 0};
-  for (int k = 0; k < n_iter; ++k) {
-    s.iter = iters[k];
-    s.tpr = 8;
-    while (s.tpr < max_tpr && s.tpr * s.iter < nvec) s.tpr *= 2;
-    if (s.tpr * s.iter >= nvec) break;
+// `iters`: the vectors a thread may hold, the wanted number first, smaller
+// ones (for few rows: more threads a row) behind it, larger ones (for rows of
+// more than 512 threads) last.
+Shape row_shape(const NormArgs& a, int vec, const int* iters, int n) {
+  const int nvec = (a.width + vec - 1) / vec;
+  const int64_t rows = a.tokens * a.heads;
+  auto at = [&](int iter) {
+    Shape s{4, 0, iter};
+    while (s.tpr < 512 && s.tpr * iter < nvec) s.tpr *= 2;
+    s.block = s.tpr <= 32 ? 128 : s.tpr;
+    return s;
+  };
+  Shape best = at(iters[0]);
+  for (int k = 1; k < n; ++k) {
+    const bool fits = best.tpr * best.iter >= nvec;
+    if (fits && (rows * best.tpr >= 148 * 256 || iters[k] > best.iter)) continue;
+    const Shape s = at(iters[k]);
+    if (!fits || s.tpr * s.iter >= nvec) best = s;
   }
-  s.block = s.tpr <= 32 ? 256 : s.tpr;
-  return s;
+  return best;
 }
 
 template <typename K>
-int resident_blocks(K kernel, int block, int sms) {
+int resident_blocks(K kernel, int block, int sms, size_t shared) {
   int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, 0) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, shared) != cudaSuccess ||
       per < 1)
     per = 1;
   return per * sms;
@@ -378,34 +779,89 @@ int resident_blocks(K kernel, int block, int sms) {
 
 template <typename IO, typename RT, int VEC, int ITER>
 cudaError_t fwd_launch(const NormArgs& a, const Shape& s, cudaStream_t stream) {
-  auto* k = norm_fwd_kernel<IO, RT, VEC, ITER>;
+  auto* k = !a.gate          ? norm_fwd_kernel<IO, RT, VEC, ITER, 0>
+            : !a.gate_first  ? norm_fwd_kernel<IO, RT, VEC, ITER, 1>
+                             : norm_fwd_kernel<IO, RT, VEC, ITER, 2>;
   const int64_t need = (a.tokens * a.heads + s.block / s.tpr - 1) / (s.block / s.tpr);
-  const int64_t most = resident_blocks(k, s.block, sm_count());
+  const int64_t most = resident_blocks(k, s.block, sm_count(), 0);
   k<<<(unsigned)(need < most ? need : most), s.block, 0, stream>>>(a, s.tpr);
   return cudaGetLastError();
+}
+
+// Shared memory of the backward for wide rows; 0 where it does not take them:
+// rows of 64 to 512 whole vectors in whole warps, a gate with a sigmoid, and
+// two slots that fit beside the weights.
+struct PairShape {
+  int threads, slot_bytes, bytes;
+};
+PairShape pair_shape(const NormArgs& a, int vec) {
+  const int threads = a.width / vec, e = a.bf16 ? 2 : 4, r = a.res_bf16 ? 2 : 4;
+  const bool pre = a.pre_weight && a.d_normed;
+  if (vec == 1 || a.width % (32 * vec) || threads < 64 || threads > 512 ||
+      (a.gate && a.act == kActNone))
+    return PairShape{0, 0, 0};
+  const int row = a.width * (e * (1 + (a.gate ? 1 : 0) + (pre ? 1 : 0)) +
+                             r * ((pre && a.residual ? 1 : 0) + (a.d_out ? 1 : 0)));
+  const PairShape s{threads, kPairRows * row, 2 * kPairRows * row + 12 * a.width};
+  return s.bytes <= 226 * 1024 ? s : PairShape{0, 0, 0};
+}
+
+// The most blocks of a backward launch: what its workspace holds parts for.
+int64_t bwd_blocks(const NormArgs& a, const Shape& s, int sms) {
+  const int per = s.block / s.tpr;
+  const int64_t need = (a.tokens * a.heads + per - 1) / per, cap = (int64_t)sms * (1024 / s.block);
+  return need < cap ? need : cap;
 }
 
 template <typename IO, typename RT, int VEC, int ITER>
 cudaError_t bwd_launch(const NormArgs& a, const Shape& s, int sms, float* part,
                        cudaStream_t stream) {
-  auto* k = norm_bwd_kernel<IO, RT, VEC, ITER>;
+  auto* k = !a.gate          ? norm_bwd_kernel<IO, RT, VEC, ITER, 0>
+            : !a.gate_first  ? norm_bwd_kernel<IO, RT, VEC, ITER, 1>
+                             : norm_bwd_kernel<IO, RT, VEC, ITER, 2>;
   const int per = s.block / s.tpr;
-  const int64_t need = (a.tokens * a.heads + per - 1) / per;
-  int64_t blocks = resident_blocks(k, s.block, sms);
-  const int64_t cap = (int64_t)sms * (2048 / s.block);
-  blocks = blocks < need ? blocks : need;
-  blocks = blocks < cap ? blocks : cap;
-  if (blocks > 0) k<<<(unsigned)blocks, s.block, 0, stream>>>(a, s.tpr, part);
-  cudaError_t e = cudaGetLastError();
+  const int bytes = per * 3 * ((a.width + 3) & ~3) * (int)sizeof(float);
+  cudaError_t e = cudaSuccess;
+  if (bytes > 47 * 1024)  // the static part comes on top
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
+  int64_t blocks = resident_blocks(k, s.block, sms, bytes);
+  const int64_t most = bwd_blocks(a, s, sms);
+  blocks = blocks < most ? blocks : most;
+  if (blocks > 0) k<<<(unsigned)blocks, s.block, bytes, stream>>>(a, s.tpr, part);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.dpost || a.dscale || a.dpre)
     norm_weight_sum_kernel<<<dim3((a.width + 31) / 32, 3), dim3(32, 16), 0, stream>>>(
         part, (int)(blocks * per), a.width, a.dpost, a.dscale, a.dpre);
   return cudaGetLastError();
 }
 
-constexpr int kVecIters[] = {1, 2, 4}, kOneIters[] = {4, 16};
-constexpr int kBwdVecIters[] = {1, 2, 4, 8}, kBwdOneIters[] = {4, 32};
+template <typename IO, typename RT, int VEC>
+cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* part,
+                        cudaStream_t stream) {
+  const bool silu = a.act == kActSilu;
+  auto* k = !a.gate ? norm_bwd_pair_kernel<IO, RT, VEC, 0, false>
+            : a.gate_first ? (silu ? norm_bwd_pair_kernel<IO, RT, VEC, 2, true>
+                                   : norm_bwd_pair_kernel<IO, RT, VEC, 2, false>)
+                           : (silu ? norm_bwd_pair_kernel<IO, RT, VEC, 1, true>
+                                   : norm_bwd_pair_kernel<IO, RT, VEC, 1, false>);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, s.bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (a.tokens * a.heads + kPairRows - 1) / kPairRows;
+  int64_t blocks = resident_blocks(k, s.threads, sms, s.bytes);
+  const int64_t cap = (int64_t)sms * (1024 / s.threads);
+  blocks = blocks < need ? blocks : need;
+  blocks = blocks < cap ? blocks : cap;
+  if (blocks > 0) k<<<(unsigned)blocks, s.threads, s.bytes, stream>>>(a, s.slot_bytes, part);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.dpost || a.dscale || a.dpre)
+    norm_weight_sum_kernel<<<dim3((a.width + 31) / 32, 3), dim3(32, 16), 0, stream>>>(
+        part, (int)blocks, a.width, a.dpost, a.dscale, a.dpre);
+  return cudaGetLastError();
+}
+
+constexpr int kFwd8[] = {4, 1}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8},
+              kOne[] = {4, 32};
 
 // 16 bytes of io a load where every pointer, stride and the width allow it,
 // single elements otherwise.
@@ -418,35 +874,40 @@ bool vec_ok(const NormArgs& a, int vec) {
 }
 
 Shape bwd_shape(const NormArgs& a, bool vec) {
-  const int v = vec ? (a.bf16 ? 8 : 4) : 1;
-  return vec ? row_shape(a.width, v, kBwdVecIters, 4, 512)
-             : row_shape(a.width, v, kBwdOneIters, 2, 512);
+  if (!vec) return row_shape(a, 1, kOne, 2);
+  return a.bf16 ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 4, kBwd4, 4);
 }
 
 template <typename IO, typename RT, int VEC>
 cudaError_t fwd_pick(const NormArgs& a, cudaStream_t st) {
-  if (VEC > 1) {
-    const Shape s = row_shape(a.width, VEC, kVecIters, 3, 1024);
+  if constexpr (VEC > 1) {
+    const Shape s = VEC == 8 ? row_shape(a, 8, kFwd8, 2) : row_shape(a, 4, kFwd4, 3);
     if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1>(a, s, st);
-    if (s.iter == 2) return fwd_launch<IO, RT, VEC, 2>(a, s, st);
-    return fwd_launch<IO, RT, VEC, 4>(a, s, st);
+    if (s.iter == 4) return fwd_launch<IO, RT, VEC, 4>(a, s, st);
+    if constexpr (VEC == 4) return fwd_launch<IO, RT, VEC, 8>(a, s, st);
+    return cudaErrorInvalidValue;
+  } else {
+    const Shape s = row_shape(a, 1, kOne, 2);
+    if (s.iter == 4) return fwd_launch<IO, RT, 1, 4>(a, s, st);
+    return fwd_launch<IO, RT, 1, 32>(a, s, st);
   }
-  const Shape s = row_shape(a.width, 1, kOneIters, 2, 1024);
-  if (s.iter == 4) return fwd_launch<IO, RT, 1, 4>(a, s, st);
-  return fwd_launch<IO, RT, 1, 16>(a, s, st);
 }
 
 template <typename IO, typename RT, int VEC>
 cudaError_t bwd_pick(const NormArgs& a, int sms, float* part, cudaStream_t st) {
   const Shape s = bwd_shape(a, VEC > 1);
-  if (VEC > 1) {
+  if constexpr (VEC > 1) {
+    if (const PairShape q = pair_shape(a, VEC); q.threads)
+      return pair_launch<IO, RT, VEC>(a, q, sms, part, st);
     if (s.iter == 1) return bwd_launch<IO, RT, VEC, 1>(a, s, sms, part, st);
     if (s.iter == 2) return bwd_launch<IO, RT, VEC, 2>(a, s, sms, part, st);
     if (s.iter == 4) return bwd_launch<IO, RT, VEC, 4>(a, s, sms, part, st);
-    return bwd_launch<IO, RT, VEC, 8>(a, s, sms, part, st);
+    if constexpr (VEC == 4) return bwd_launch<IO, RT, VEC, 8>(a, s, sms, part, st);
+    return cudaErrorInvalidValue;
+  } else {
+    if (s.iter == 4) return bwd_launch<IO, RT, 1, 4>(a, s, sms, part, st);
+    return bwd_launch<IO, RT, 1, 32>(a, s, sms, part, st);
   }
-  if (s.iter == 4) return bwd_launch<IO, RT, 1, 4>(a, s, sms, part, st);
-  return bwd_launch<IO, RT, 1, 32>(a, s, sms, part, st);
 }
 
 }  // namespace
@@ -462,11 +923,14 @@ cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
 
 size_t norm_bwd_workspace_bytes(const NormArgs& a, int sms) {
   if (!a.dpost && !a.dscale && !a.dpre) return 0;
-  const Shape s = bwd_shape(a, vec_ok(a, a.bf16 ? 8 : 4));
-  const int per = s.block / s.tpr;
-  const int64_t need = (a.tokens * a.heads + per - 1) / per;
-  const int64_t cap = (int64_t)sms * (2048 / s.block);
-  return (size_t)(need < cap ? need : cap) * per * 3 * a.width * sizeof(float);
+  const bool vec = vec_ok(a, a.bf16 ? 8 : 4);
+  if (const PairShape q = pair_shape(a, vec ? (a.bf16 ? 8 : 4) : 1); q.threads) {
+    const int64_t need = (a.tokens * a.heads + kPairRows - 1) / kPairRows,
+                  cap = (int64_t)sms * (1024 / q.threads);
+    return (size_t)(need < cap ? need : cap) * 3 * a.width * sizeof(float);
+  }
+  const Shape s = bwd_shape(a, vec);
+  return (size_t)bwd_blocks(a, s, sms) * (s.block / s.tpr) * 3 * a.width * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, void* ws, int sms, cudaStream_t st) {
