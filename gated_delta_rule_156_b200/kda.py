@@ -587,67 +587,75 @@ class _On:
     call runs with that device current, and what it allocates belongs to that
     stream, so it may be made from any device or stream; the caller orders
     the stream behind whatever wrote the inputs."""
+    __slots__ = ("dev", "stream", "old_dev", "old_stream")
 
-    def __init__(self, t, stream):
-        self.dev, self.stream = t.device, stream
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
 
     def __enter__(self):
+        dev, stream = self.dev, self.stream
         self.old_dev = self.old_stream = None
-        if self.dev.index != torch.cuda.current_device():
+        if dev != torch.cuda.current_device():
             self.old_dev = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        cur = torch.cuda.current_stream(self.dev)
-        if self.stream is not None and self.stream != cur:
-            if self.stream.device != self.dev:
-                self._leave()
+            torch.cuda.set_device(dev)
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(dev)
+        cur = torch.cuda.current_stream(dev)
+        if stream != cur:
+            if stream.device_index != dev:
+                self.__exit__()
                 raise ValueError("the stream must be on the tensors' device")
             self.old_stream = cur
-            torch.cuda.set_stream(self.stream)
-            cur = self.stream
-        return cur.cuda_stream
+            torch.cuda.set_stream(stream)
+        return stream.cuda_stream
 
-    def _leave(self):
+    def __exit__(self, *exc):
         if self.old_stream is not None:
             torch.cuda.set_stream(self.old_stream)
         if self.old_dev is not None:
             torch.cuda.set_device(self.old_dev)
 
-    def __exit__(self, *exc):
-        self._leave()
+
+def _device(name, t, dims=0):
+    """The device index of a call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dims and t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got "
+                         f"{tuple(t.shape)}")
+    return t.get_device()
 
 
-def _need(name, t, dev, dtype, shape, optional=False):
-    """A dense tensor of this dtype and shape on dev (None where optional)."""
-    if t is None:
-        if optional:
-            return
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, torch.Tensor) or t.device != dev or \
-            dev.type != "cuda":
+def _is(name, t, dev, dtype, shape):
+    """Checks a tensor's device, dtype and shape."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and \
+            t.dtype is dtype and t.shape == shape:
+        return
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on one device with "
                          "the others")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got "
+                     f"{tuple(t.shape)}")
+
+
+def _need(name, t, dev, dtype, shape, optional=False):
+    """Checks a dense tensor of this dtype and shape (None where optional)."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    _is(name, t, dev, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _tokens(name, t, dev, dtype, shape, inner=1):
-    """A tensor of this shape whose leading dims are tokens and whose last
-    `inner` dims are one token's elements: dense within a token, tokens at one
-    stride (a slice of a wider tensor will do).  Returns the stride."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or \
-            dev.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on one device with "
-                         "the others")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)}")
+    """Checks a tensor of this shape whose leading dims are tokens and whose
+    last `inner` dims are one token's elements: dense within a token, tokens
+    at one stride (a slice of a wider tensor will do).  Returns the stride."""
+    _is(name, t, dev, dtype, shape)
     if t.is_contiguous() or t.numel() == 0:
         return 0
     stride = _token_stride(t, inner)
@@ -684,13 +692,7 @@ def _token_stride(t, inner):
 
 def _groups(name, t, dev, dtype, shape):
     """(token stride, group stride) of B or C [B, T, G, S]."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or \
-            dev.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on one device with "
-                         "the others")
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
+    _is(name, t, dev, dtype, shape)
     if t.is_contiguous() or t.numel() == 0:
         return 0, 0
     b, n, g, s = shape
@@ -707,45 +709,43 @@ def _groups(name, t, dev, dtype, shape):
     return token, group
 
 
-def _batch(x, cu_seqlens, name):
-    """(B, T, sequences) of a [B, T, ...] tensor, dense or packed."""
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or \
-            x.dim() < 3:
-        raise ValueError(f"{name} must be a CUDA tensor [B, T, ...]")
-    B, T = x.shape[:2]
+def _sequences(x, dev, cu_seqlens):
+    """Sequences of a [B, T, ...] tensor, dense or packed, and the n_seqs that
+    its shape struct takes."""
     if cu_seqlens is None:
-        return B, T, B
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        return x.shape[0], 0
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or \
+            cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must hold n_seqs + 1 offsets")
-    if B != 1:
+    if x.shape[0] != 1:
         raise ValueError("a packed batch has B == 1")
     n = cu_seqlens.numel() - 1
-    _need("cu_seqlens", cu_seqlens, x.device, torch.int32, (n + 1,))
-    return B, T, n
+    _need("cu_seqlens", cu_seqlens, dev, torch.int32, (n + 1,))
+    return n, n
 
 
 def _run(name, shape, tensors, stream):
-    fn = getattr(library(), name)
-    st = fn(ctypes.byref(shape),
-            *[None if t is None else t.data_ptr() for t in tensors], stream)
+    st = getattr(library(), name)(
+        ctypes.byref(shape),
+        *[None if t is None else t.data_ptr() for t in tensors], stream)
     if st != KDA_OK:
         raise KdaError(st, name)
 
 
 def _conv_shape(x, weight, bias, cu_seqlens, activation):
-    B, T, n = _batch(x, cu_seqlens, "x")
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, D]")
-    D, dev, f32 = x.shape[2], x.device, torch.float32
+    """(shape struct, device, dims of x, dims of the states)"""
+    dev, f32 = _device("x", x, 3), torch.float32
+    full = x.shape
+    n, packed = _sequences(x, dev, cu_seqlens)
+    B, T, D = full
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [D, W]")
     W = weight.shape[1]
     _need("weight", weight, dev, f32, (D, W))
     _need("bias", bias, dev, f32, (D,), optional=True)
-    stride = _tokens("x", x, dev, x.dtype, x.shape)
-    shape = KdaConvShape(B, T, D, W, n if cu_seqlens is not None else 0,
-                         _io(x), ACTS[activation], stride)
-    return shape, (B, T, D), (n, W - 1, D)
+    shape = KdaConvShape(B, T, D, W, packed, _io(x), ACTS[activation],
+                         _tokens("x", x, dev, x.dtype, full))
+    return shape, dev, full, (n, W - 1, D)
 
 
 def short_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None,
@@ -758,15 +758,15 @@ def short_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None,
     initial_state [N, W-1, D] like x or None (zeros), activation "silu" or
     "none".  Returns (out [B, T, D], final_state [N, W-1, D] or None).
     """
-    shape, full, state = _conv_shape(x, weight, bias, cu_seqlens, activation)
-    dev, dt = x.device, x.dtype
+    shape, dev, full, state = _conv_shape(x, weight, bias, cu_seqlens,
+                                          activation)
+    dt = x.dtype
     _need("initial_state", initial_state, dev, dt, state, optional=True)
     _need("out", out, dev, dt, full, optional=True)
-    with _On(x, stream) as s:
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(full, dtype=dt, device=dev)
-        final = torch.empty(state, dtype=dt, device=dev) \
-            if want_final_state else None
+            out = x.new_empty(full)
+        final = x.new_empty(state) if want_final_state else None
         _run("kda_short_conv_fwd", shape,
              (x, weight, bias, initial_state, cu_seqlens, out, final), s)
     return out, final
@@ -777,17 +777,17 @@ def short_conv_bwd(x, weight, bias, initial_state, cu_seqlens, d_out,
                    want_initial_state=True, stream=None):
     """Gradients of short_conv_fwd (kda_short_conv_bwd): (dx, d_weight,
     d_bias or None, d_initial_state or None)."""
-    shape, full, state = _conv_shape(x, weight, bias, cu_seqlens, activation)
-    dev, dt = x.device, x.dtype
+    shape, dev, full, state = _conv_shape(x, weight, bias, cu_seqlens,
+                                          activation)
+    dt = x.dtype
     _need("initial_state", initial_state, dev, dt, state, optional=True)
     _need("d_out", d_out, dev, dt, full)
     _need("d_final_state", d_final_state, dev, dt, state, optional=True)
-    with _On(x, stream) as s:
-        dx = torch.empty(full, dtype=dt, device=dev)
+    with _On(dev, stream) as s:
+        dx = x.new_empty(full)
         dw = torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
-        d0 = torch.empty(state, dtype=dt, device=dev) \
-            if want_initial_state else None
+        d0 = x.new_empty(state) if want_initial_state else None
         _run("kda_short_conv_bwd", shape,
              (x, weight, bias, initial_state, cu_seqlens, d_out,
               d_final_state, dx, dw, db, d0), s)
@@ -798,36 +798,38 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None,
                     stream=None):
     """The convolution of T >= 1 new tokens (kda_short_conv_step): x
     [N, T, D]; ``state`` [N, W-1, D] is updated in place.  Returns out."""
-    shape, full, st = _conv_shape(x, weight, bias, None, activation)
-    dev, dt = x.device, x.dtype
+    shape, dev, full, st = _conv_shape(x, weight, bias, None, activation)
+    dt = x.dtype
     _need("state", state, dev, dt, st)
     _need("out", out, dev, dt, full, optional=True)
-    with _On(x, stream) as s:
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(full, dtype=dt, device=dev)
+            out = x.new_empty(full)
         _run("kda_short_conv_step", shape, (x, weight, bias, state, out), s)
     return out
 
 
 def _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias, cu_seqlens, softplus):
-    B, T, n = _batch(u, cu_seqlens, "u")
-    if u.dim() != 3 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
+    """(shape struct, device, dims of u, dims of the states)"""
+    dev, dt, f32 = _device("u", u, 3), u.dtype, torch.float32
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or \
             not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
-        raise ValueError("u must be [B, T, D], A [D, S], Bm [B, T, G, S]")
-    C, S, G = u.shape[2], A.shape[1], Bm.shape[2]
-    dev, dt, f32 = u.device, u.dtype, torch.float32
+        raise ValueError("A must be [D, S], Bm [B, T, G, S]")
+    full = u.shape
+    n, packed = _sequences(u, dev, cu_seqlens)
+    B, T, C = full
+    S, G = A.shape[1], Bm.shape[2]
     _need("A", A, dev, f32, (C, S))
     _need("D", D, dev, f32, (C,), optional=True)
     _need("delta_bias", delta_bias, dev, f32, (C,), optional=True)
-    us = _tokens("u", u, dev, dt, u.shape)
-    ds = _tokens("delta", delta, dev, dt, u.shape)
-    zs = 0 if z is None else _tokens("z", z, dev, dt, u.shape)
+    us = _tokens("u", u, dev, dt, full)
+    ds = _tokens("delta", delta, dev, dt, full)
+    zs = 0 if z is None else _tokens("z", z, dev, dt, full)
     bs, bg = _groups("Bm", Bm, dev, dt, (B, T, G, S))
     cs, cg = _groups("Cm", Cm, dev, dt, (B, T, G, S))
-    shape = KdaSsmShape(B, T, C, S, G, n if cu_seqlens is not None else 0,
-                        _io(u), int(bool(softplus)), us, ds, zs, bs, bg, cs,
-                        cg)
-    return shape, (n, C, S)
+    shape = KdaSsmShape(B, T, C, S, G, packed, _io(u), 1 if softplus else 0,
+                        us, ds, zs, bs, bg, cs, cg)
+    return shape, dev, full, (n, C, S)
 
 
 def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
@@ -841,17 +843,17 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
     Returns (out [B, T, D], final_state [N, D, S] fp32); ``final_state`` may
     be the initial state itself.
     """
-    shape, state = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias,
-                              cu_seqlens, softplus)
-    dev, dt, f32 = u.device, u.dtype, torch.float32
+    shape, dev, full, state = _ssm_shape(u, delta, A, Bm, Cm, D, z,
+                                         delta_bias, cu_seqlens, softplus)
+    dt, f32 = u.dtype, torch.float32
     _need("initial_state", initial_state, dev, f32, state, optional=True)
-    _need("out", out, dev, dt, u.shape, optional=True)
+    _need("out", out, dev, dt, full, optional=True)
     _need("final_state", final_state, dev, f32, state, optional=True)
-    with _On(u, stream) as s:
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(u.shape, dtype=dt, device=dev)
+            out = u.new_empty(full)
         if final_state is None:
-            final_state = torch.empty(state, dtype=f32, device=dev)
+            final_state = A.new_empty(state)
         _run("kda_ssm_scan_fwd", shape,
              (u, delta, A, Bm, Cm, D, z, delta_bias, initial_state,
               cu_seqlens, out, final_state), s)
@@ -865,23 +867,20 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
     """Gradients of ssm_scan_fwd (kda_ssm_scan_bwd): (du, d_delta, dA, dBm,
     dCm, dD, dz, d_delta_bias, d_initial_state), None where the input is
     None (d_initial_state: unless want_initial_state)."""
-    shape, state = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias,
-                              cu_seqlens, softplus)
-    dev, dt, f32 = u.device, u.dtype, torch.float32
+    shape, dev, full, state = _ssm_shape(u, delta, A, Bm, Cm, D, z,
+                                         delta_bias, cu_seqlens, softplus)
+    dt, f32 = u.dtype, torch.float32
     _need("initial_state", initial_state, dev, f32, state, optional=True)
-    _need("d_out", d_out, dev, dt, u.shape)
+    _need("d_out", d_out, dev, dt, full)
     _need("d_final_state", d_final_state, dev, f32, state, optional=True)
-    with _On(u, stream) as s:
-        du = torch.empty(u.shape, dtype=dt, device=dev)
-        dd = torch.empty(u.shape, dtype=dt, device=dev)
+    with _On(dev, stream) as s:
+        du, dd = u.new_empty(full), u.new_empty(full)
         dA = torch.empty_like(A)
-        dB = torch.empty(Bm.shape, dtype=dt, device=dev)
-        dC = torch.empty(Bm.shape, dtype=dt, device=dev)
+        dB, dC = u.new_empty(Bm.shape), u.new_empty(Bm.shape)
         dD = None if D is None else torch.empty_like(D)
-        dz = None if z is None else torch.empty(u.shape, dtype=dt, device=dev)
+        dz = None if z is None else u.new_empty(full)
         db = None if delta_bias is None else torch.empty_like(delta_bias)
-        d0 = torch.empty(state, dtype=f32, device=dev) \
-            if want_initial_state else None
+        d0 = A.new_empty(state) if want_initial_state else None
         _run("kda_ssm_scan_bwd", shape,
              (u, delta, A, Bm, Cm, D, z, delta_bias, initial_state,
               cu_seqlens, d_out, d_final_state, du, dd, dA, dB, dC, dD, dz,
@@ -906,14 +905,14 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None,
     """The scan over T >= 1 new tokens (kda_ssm_step): u, delta, z [N, T, D],
     Bm, Cm [N, T, G, S]; ``state`` [N, D, S] fp32 is updated in place.
     Returns out [N, T, D]."""
-    shape, st = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias, None,
-                           softplus)
-    dev, dt = u.device, u.dtype
+    shape, dev, full, st = _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias,
+                                      None, softplus)
+    dt = u.dtype
     _need("state", state, dev, torch.float32, st)
-    _need("out", out, dev, dt, u.shape, optional=True)
-    with _On(u, stream) as s:
+    _need("out", out, dev, dt, full, optional=True)
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(u.shape, dtype=dt, device=dev)
+            out = u.new_empty(full)
         _run("kda_ssm_step", shape,
              (u, delta, A, Bm, Cm, D, z, delta_bias, state, out), s)
     return out
@@ -921,13 +920,11 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None,
 
 def _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
                 gate_act, gate_first, eps):
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or \
-            x.dim() < 2:
-        raise ValueError("x must be a CUDA tensor [..., width]")
-    dev, dt, f32 = x.device, x.dtype, torch.float32
+    """(shape struct, device)"""
+    dev, dt, f32 = _device("x", x), x.dtype, torch.float32
+    if x.dim() < 2 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., width]")
     width = x.shape[-1]
-    if width == 0:
-        raise ValueError("x must have a width")
     # rows at one stride, else tokens of `heads` dense rows at one stride
     inner = 1
     for t in (x, gate):
@@ -946,8 +943,8 @@ def _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
         raise ValueError(f"the residual must be {dt} or float32, got {rt}")
     return KdaNormShape(tokens, max(heads, 1), width, _io(x),
                         KDA_BF16 if rt == torch.bfloat16 else KDA_F32,
-                        ACTS[gate_act], int(bool(gate_first)), float(eps), xs,
-                        gs)
+                        ACTS[gate_act], 1 if gate_first else 0, eps, xs,
+                        gs), dev
 
 
 def block_norm_fwd(x, post_weight=None, gate=None, residual=None, scale=None,
@@ -969,16 +966,16 @@ def block_norm_fwd(x, post_weight=None, gate=None, residual=None, scale=None,
     """
     rt = residual.dtype if isinstance(residual, torch.Tensor) else \
         out.dtype if isinstance(out, torch.Tensor) else x.dtype
-    shape = _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
-                        gate_act, gate_first, eps)
-    dev, dt = x.device, x.dtype
+    shape, dev = _norm_shape(x, post_weight, gate, residual, scale,
+                             pre_weight, rt, gate_act, gate_first, eps)
+    dt = x.dtype
     _need("out", out, dev, rt, x.shape, optional=True)
     _need("normed", normed, dev, dt, x.shape, optional=True)
-    with _On(x, stream) as s:
+    with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(x.shape, dtype=rt, device=dev)
+            out = x.new_empty(x.shape, dtype=rt)
         if normed is None and pre_weight is not None:
-            normed = torch.empty(x.shape, dtype=dt, device=dev)
+            normed = x.new_empty(x.shape)
         _run("kda_block_norm_fwd", shape,
              (x, post_weight, gate, residual, scale, pre_weight, out, normed),
              s)
@@ -995,16 +992,15 @@ def block_norm_bwd(x, post_weight=None, gate=None, residual=None, scale=None,
     (zero)."""
     rt = residual.dtype if isinstance(residual, torch.Tensor) else \
         d_out.dtype if isinstance(d_out, torch.Tensor) else x.dtype
-    shape = _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
-                        gate_act, gate_first, eps)
-    dev, dt = x.device, x.dtype
+    shape, dev = _norm_shape(x, post_weight, gate, residual, scale,
+                             pre_weight, rt, gate_act, gate_first, eps)
+    dt = x.dtype
     _need("d_out", d_out, dev, rt, x.shape, optional=True)
     _need("d_normed", d_normed, dev, dt, x.shape, optional=True)
 
     def like(t, dtype):
-        return None if t is None else torch.empty(t.shape, dtype=dtype,
-                                                  device=dev)
-    with _On(x, stream) as s:
+        return None if t is None else x.new_empty(t.shape, dtype=dtype)
+    with _On(dev, stream) as s:
         dx, dg, dr = like(x, dt), like(gate, dt), like(residual, rt)
         f32 = torch.float32
         dpost, dscale, dpre = (like(t, f32) for t in
