@@ -407,71 +407,102 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   }
 }
 
-// New tokens: L lanes own a channel of a sequence and stream its state, read
-// and written once per call.
-template <typename IO, int L>
+// New tokens: L lanes own a channel and stream the states of NS sequences, read
+// and written once per call; A is read once for all of them, and each lane
+// forms the step and the result of one of the sequences.  VEC: 4 states of B,
+// C and the state are one access each.  Bound by HBM.
+template <typename IO, int L, int NS, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
-  const int l = threadIdx.x % L;
-  const int64_t id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
-  const bool on = id < (int64_t)a.n_seqs * a.D;
-  const int64_t at = on ? id : 0;
-  const int seq = (int)(at / a.D), d = (int)(at - (int64_t)seq * a.D);
-  const int g = d / (a.D / a.G);
-  float A2[kSsmStates], h[kSsmStates];
-  const bool vec = (a.S & 3) == 0;
-  float* st = a.h_out + at * a.S + l * kSsmStates;
-  const bool real4 = on && l * kSsmStates < a.S;
-  if (vec) {
-    const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 hv = real4 ? *reinterpret_cast<const float4*>(st) : z4;
-    const float4 av = real4 ? *reinterpret_cast<const float4*>(
-                                  a.A + (int64_t)d * a.S + l * kSsmStates) : z4;
-    h[0] = hv.x; h[1] = hv.y; h[2] = hv.z; h[3] = hv.w;
-    A2[0] = av.x; A2[1] = av.y; A2[2] = av.z; A2[3] = av.w;
-  } else {
+  constexpr int SL = kSsmStates;
+  const int l = threadIdx.x % L, n0 = l * SL;
+  const int dd = (blockIdx.x * 256 + threadIdx.x) / L;
+  const bool mine = dd < a.D;
+  const int d = mine ? dd : 0, g = d / (a.D / a.G);
+  float A2[SL];
 #pragma unroll
-    for (int i = 0; i < kSsmStates; ++i) {
-      const bool real = on && l * kSsmStates + i < a.S;
-      h[i] = real ? st[i] : 0.f;
-      A2[i] = real ? a.A[(int64_t)d * a.S + l * kSsmStates + i] : 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kSsmStates; ++i) A2[i] *= kLog2e;
+  for (int i = 0; i < SL; ++i)
+    A2[i] = mine && n0 + i < a.S ? a.A[(int64_t)d * a.S + n0 + i] * kLog2e : 0.f;
   const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
-  for (int t = 0; t < a.T; ++t) {
-    const int64_t tok = (int64_t)seq * a.T + t;
-    const float raw = to_f32(static_cast<const IO*>(a.delta)[tok * a.delta_stride + d]) + bias;
-    const float uu = to_f32(static_cast<const IO*>(a.u)[tok * a.u_stride + d]);
-    const IO* B = static_cast<const IO*>(a.B) + tok * a.b_stride + (int64_t)g * a.b_group;
-    const IO* C = static_cast<const IO*>(a.C) + tok * a.c_stride + (int64_t)g * a.c_group;
-    const float dt = a.softplus ? softplus_f(raw) : raw, dtu = dt * uu;
-    float y = 0.f;
+  const IO* B = static_cast<const IO*>(a.B) + g * a.b_group + n0;
+  const IO* C = static_cast<const IO*>(a.C) + g * a.c_group + n0;
+  const bool lane_on = mine && n0 < a.S;
+  // where SpreadSum leaves sequence k's sum
+  const int own = NS == 4 ? (l & 1) * 2 + (l >> 1 & 1) : l % NS;
+  for (int s0 = blockIdx.y * NS; s0 < a.n_seqs; s0 += gridDim.y * NS) {
+    float h[NS][SL];
 #pragma unroll
-    for (int i = 0; i < kSsmStates; ++i) {
-      const int n = l * kSsmStates + i;
-      if (n < a.S) {
-        h[i] = fmaf(ex2_f(dt * A2[i]), h[i], dtu * to_f32(B[n]));
-        y = fmaf(h[i], to_f32(C[n]), y);
+    for (int k = 0; k < NS; ++k) {
+      const float* st = a.h_out + ((int64_t)(s0 + k) * a.D + d) * a.S + n0;
+      const bool on = lane_on && s0 + k < a.n_seqs;
+      if (VEC) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) v = __ldcs(reinterpret_cast<const float4*>(st));
+        h[k][0] = v.x; h[k][1] = v.y; h[k][2] = v.z; h[k][3] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < SL; ++i) h[k][i] = on && n0 + i < a.S ? st[i] : 0.f;
+      }
+    }
+    for (int t = 0; t < a.T; ++t) {
+      Held<IO, SL, VEC> rb[NS], rc[NS];
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        const int64_t tok = (int64_t)min(s0 + k, a.n_seqs - 1) * a.T + t;
+        rb[k].clear();
+        rc[k].clear();
+        if (VEC) {
+          if (n0 < a.S) {
+            rb[k].all(B + tok * a.b_stride);
+            rc[k].all(C + tok * a.c_stride);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < SL; ++i)
+            if (n0 + i < a.S) {
+              rb[k].one(i, B + tok * a.b_stride + i);
+              rc[k].one(i, C + tok * a.c_stride + i);
+            }
+        }
+      }
+      // the step and the result of sequence `own` are this lane's
+      const int64_t tok = (int64_t)min(s0 + own, a.n_seqs - 1) * a.T + t;
+      const float raw = to_f32(static_cast<const IO*>(a.delta)[tok * a.delta_stride + d]) + bias;
+      const float uu = to_f32(static_cast<const IO*>(a.u)[tok * a.u_stride + d]);
+      const float gz = a.z ? to_f32(static_cast<const IO*>(a.z)[tok * a.z_stride + d]) : 0.f;
+      const float dt0 = a.softplus ? softplus_f(raw) : raw, dtu0 = dt0 * uu;
+      float y[NS];
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        const int from = NS == 4 ? (k >> 1) | (k & 1) << 1 : k;  // the lane with own == k
+        const float dt = NS == 1 ? dt0 : __shfl_sync(0xffffffffu, dt0, from, L);
+        const float dtu = NS == 1 ? dtu0 : __shfl_sync(0xffffffffu, dtu0, from, L);
+        y[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+          h[k][i] = fmaf(ex2_f(dt * A2[i]), h[k][i], dtu * rb[k].get(i));
+          y[k] = fmaf(h[k][i], rc[k].get(i), y[k]);
+        }
+      }
+      int f = 0;
+      SpreadSum<NS, 1, L>::run(y, l, f);
+      if (mine && l < NS && s0 + own < a.n_seqs) {
+        float r = fmaf(skip, uu, y[0]);
+        if (a.z) r *= gz * sigmoid_f(gz);
+        static_cast<IO*>(a.out)[tok * a.D + d] = from_f32<IO>(r);
       }
     }
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (on && l == 0) {
-      y = fmaf(skip, uu, y);
-      if (a.z) {
-        const float gz = to_f32(static_cast<const IO*>(a.z)[tok * a.z_stride + d]);
-        y *= gz * sigmoid_f(gz);
-      }
-      static_cast<IO*>(a.out)[tok * a.D + d] = from_f32<IO>(y);
-    }
-  }
-  if (vec) {
-    if (real4) *reinterpret_cast<float4*>(st) = make_float4(h[0], h[1], h[2], h[3]);
-  } else {
+    for (int k = 0; k < NS; ++k) {
+      float* st = a.h_out + ((int64_t)(s0 + k) * a.D + d) * a.S + n0;
+      if (!lane_on || s0 + k >= a.n_seqs) continue;
+      if (VEC) {
+        __stcs(reinterpret_cast<float4*>(st), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
+      } else {
 #pragma unroll
-    for (int i = 0; i < kSsmStates; ++i)
-      if (on && l * kSsmStates + i < a.S) st[i] = h[i];
+        for (int i = 0; i < SL; ++i)
+          if (n0 + i < a.S) st[i] = h[k][i];
+      }
+    }
   }
 }
 
@@ -520,8 +551,19 @@ cudaError_t fwd_pick(const SsmArgs& a, const SsmSave& save, const SsmSplit& spli
 
 template <typename IO, int L>
 cudaError_t step_launch(const SsmArgs& a, cudaStream_t st) {
-  const int64_t threads = (int64_t)a.n_seqs * a.D * L;
-  ssm_step_kernel<IO, L><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
+  // four sequences a thread (two for two lanes) where that still fills the SMs
+  constexpr int NS = L >= 4 ? 4 : 2;
+  const bool many = (int64_t)a.n_seqs * a.D * L >= (int64_t)4 * 148 * 2048;
+  const int ns = many ? NS : 1;
+  const bool vec = a.S % 4 == 0 && a.b_stride % 4 == 0 && a.c_stride % 4 == 0 &&
+                   a.b_group % 4 == 0 && a.c_group % 4 == 0 && aligned_to(a.h_out, 16) &&
+                   aligned_to(a.B, 4 * sizeof(IO)) && aligned_to(a.C, 4 * sizeof(IO));
+  const int64_t groups = (a.n_seqs + ns - 1) / ns;
+  const dim3 grid((unsigned)(((int64_t)a.D * L + 255) / 256),
+                  (unsigned)(groups < 65535 ? groups : 65535));
+  auto* k = many ? (vec ? ssm_step_kernel<IO, L, NS, true> : ssm_step_kernel<IO, L, NS, false>)
+                 : (vec ? ssm_step_kernel<IO, L, 1, true> : ssm_step_kernel<IO, L, 1, false>);
+  k<<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
