@@ -169,6 +169,11 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   return r;
 }
 __device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
 __device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
   float a, b;
   unpack2(mul2(x, both(-kLog2e)), a, b);

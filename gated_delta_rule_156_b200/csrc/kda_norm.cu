@@ -46,12 +46,6 @@ struct Gate {
   }
 };
 
-__device__ __forceinline__ float sum2(f32x2 v) {
-  float lo, hi;
-  unpack2(v, lo, hi);
-  return lo + hi;
-}
-
 // Sums of N <= 4 values over the TPR threads of a row, in every one of them.
 // TPR <= 32: exchanges.  Above, the row is the whole block: per-warp sums
 // through shared memory; `turn` alternates between two buffers, so that one

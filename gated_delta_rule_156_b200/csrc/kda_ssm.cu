@@ -12,12 +12,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kHelpers = 128;     // helper threads
 constexpr int kMinSegment = 128;  // tokens: below, a split's passes are all latency
-
-// Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
-// (a helper then holds 8 pairs as with four lanes, and nothing spills).
-constexpr int tile_of(int lanes) { return lanes == 2 ? 16 : 32; }
 
 // A CTA's shared memory, two of each: the tile in work and the next.
 template <int L, bool WANT_Y>
@@ -28,54 +23,6 @@ struct FwdShared {
   float b[2][TILE][SW];
   float c[2][WANT_Y ? TILE : 1][SW];
   float y[2][WANT_Y ? TILE : 1][YP];
-};
-
-// N elements on their way from memory, as the 32-bit registers that the loads
-// write: nothing touches them before get(), so that every load of a tile is
-// in flight at once.  VEC: neighbouring elements, aligned to their whole size
-// (16 bytes at most), else one register each.
-template <typename IO, int N, bool VEC>
-struct Held {
-  static constexpr int BYTES = N * (int)sizeof(IO);
-  static constexpr bool PACKED = VEC && BYTES % 4 == 0;
-  static constexpr int WORDS = PACKED ? BYTES / 4 : N;
-  static constexpr int ALIGN = VEC ? (BYTES > 16 ? 16 : BYTES) : (int)sizeof(IO);
-  uint32_t w[WORDS];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) w[i] = 0;
-  }
-  __device__ __forceinline__ void one(int j, const IO* p) {
-    if constexpr (sizeof(IO) == 2)
-      w[j] = *reinterpret_cast<const uint16_t*>(p);
-    else
-      w[j] = *reinterpret_cast<const uint32_t*>(p);
-  }
-  __device__ __forceinline__ void all(const IO* p) {
-    if constexpr (!PACKED) {
-      one(0, p);
-    } else if constexpr (WORDS == 1) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (WORDS == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < WORDS; i += 4) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
-        w[i] = v.x;
-        w[i + 1] = v.y;
-        w[i + 2] = v.z;
-        w[i + 3] = v.w;
-      }
-    }
-  }
-  __device__ __forceinline__ float get(int j) const {
-    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[j]);
-    if constexpr (!PACKED) return __uint_as_float(w[j] << 16);
-    return j & 1 ? bf_hi(w[j / 2]) : bf_lo(w[j / 2]);
-  }
 };
 
 // CTA: 4 warps run the recurrence, 4 helper warps feed them and finish their
@@ -230,10 +177,14 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         for (int j = 0; j < E; ++j)
           s_dt[w][tok_of(j)][slot(tok_of(j), ch_of(j))] = make_float2(dt[j], dtu[j]);
       }
+      float v[BN];
 #pragma unroll
-      for (int j = 0; j < BN; ++j) {
-        s_b[w][bt][bn + j] = ONE || bc_vec ? r.b.get(j) : r.b1.get(j);
-        if (WANT_Y) s_c[w][bt][bn + j] = ONE || bc_vec ? r.c.get(j) : r.c1.get(j);
+      for (int j = 0; j < BN; ++j) v[j] = ONE || bc_vec ? r.b.get(j) : r.b1.get(j);
+      store_floats<BN>(&s_b[w][bt][bn], v);
+      if (WANT_Y) {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) v[j] = ONE || bc_vec ? r.c.get(j) : r.c1.get(j);
+        store_floats<BN>(&s_c[w][bt][bn], v);
       }
     };
     auto finish = [&](int i, const float (&add_)[E], const float (&mul_)[E]) {

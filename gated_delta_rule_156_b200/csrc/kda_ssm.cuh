@@ -18,6 +18,75 @@ namespace kda {
 
 constexpr int kSsmThreads = 128;
 constexpr int kSsmStates = 4;  // states per lane
+constexpr int kHelpers = 128;  // threads that feed the recurrence's 128
+
+// Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
+// (a helper then holds 8 pairs as with four lanes, and nothing spills).
+constexpr int tile_of(int lanes) { return lanes == 2 ? 16 : 32; }
+
+// N elements on their way from memory, as the 32-bit registers that the loads
+// write: nothing touches them before get(), so that every load of a tile is
+// in flight at once.  VEC: neighbouring elements, aligned to their whole size
+// (16 bytes at most), else one register each.
+template <typename IO, int N, bool VEC>
+struct Held {
+  static constexpr int BYTES = N * (int)sizeof(IO);
+  static constexpr bool PACKED = VEC && BYTES % 4 == 0;
+  static constexpr int WORDS = PACKED ? BYTES / 4 : N;
+  static constexpr int ALIGN = VEC ? (BYTES > 16 ? 16 : BYTES) : (int)sizeof(IO);
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void one(int j, const IO* p) {
+    if constexpr (sizeof(IO) == 2)
+      w[j] = *reinterpret_cast<const uint16_t*>(p);
+    else
+      w[j] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void all(const IO* p) {
+    if constexpr (!PACKED) {
+      one(0, p);
+    } else if constexpr (WORDS == 1) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (WORDS == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; i += 4) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = v.x;
+        w[i + 1] = v.y;
+        w[i + 2] = v.z;
+        w[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[j]);
+    if constexpr (!PACKED) return __uint_as_float(w[j] << 16);
+    return j & 1 ? bf_hi(w[j / 2]) : bf_lo(w[j / 2]);
+  }
+};
+
+// N consecutive floats to shared memory (aligned to 4 N bytes, 16 at most).
+template <int N>
+__device__ __forceinline__ void store_floats(float* p, const float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = v[i];
+  }
+}
+
 // The channels of a CTA: channel blocks are counted group by group.
 struct SsmBlock {
   int g, c0, n;  // group, first channel, channels (<= CH)

@@ -21,185 +21,447 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdParts {
-  float* states;  // [chunk ids][D][S]
+  float* states;  // [piece ids of 8 tokens][D][S]
   float* bc;      // [channel block][token][2][S]
   float* dA;      // [n_seqs][D][S]
   float* dskip;   // [n_seqs][D]
   float* dbias;   // [n_seqs][D]
 };
 
-template <typename IO, int L>
-__global__ void __launch_bounds__(kSsmThreads) ssm_bwd_kernel(SsmBwdArgs b, BwdParts part) {
-  constexpr int CH = kSsmThreads / L, SW = L * kSsmStates, K = kSsmChunk;
-  constexpr int WARPS = kSsmThreads / 32;
+// D += A B of one warp, 16 x 8 by 8 x 8, in tf32 with fp32 sums.  The operands'
+// bits are used as they are: the tensor cores read the upper 10 bits of the
+// mantissa.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, float b0, float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+template <int L>
+struct BwdShared {
+  static constexpr int TILE = tile_of(L), CH = kSsmThreads / L, SW = L * kSsmStates;
+  static constexpr int YP = CH + 8;
+  static constexpr int WARPS = kSsmThreads / 32;
+  // one buffer of the warps' sums where two would not fit (S > 64); the tile
+  // then waits for the helpers to have read the last one's
+  static constexpr int PARTS = L == 32 ? 1 : 2;
+  float2 dt[2][TILE][CH];              // step, step * u
+  float dy[2][TILE][CH];
+  float b[2][TILE][SW], c[2][TILE][SW];
+  float fed[2][TILE][YP], qa[2][TILE][YP];
+  float part[PARTS][WARPS][TILE][2][SW];  // a warp's dB and dC
+  float4 state[2][TILE / kSsmChunk][kSsmThreads];
+};
+
+// Like the forward's CTA (see kda_ssm.cu): 4 warps run the recurrence, here
+// tile by tile from the end, 4 helper warps turn the next tile into step, step
+// * u, dy, B and C and finish the previous one.  A recurrence thread's start
+// states of a tile's chunks come by asynchronous copies of its own, a tile
+// ahead.
+//
+// Per chunk of 8 tokens a thread runs its 4 states forward, keeping them and
+// their decays in registers, and then back.  The sums over channels (dB, dC)
+// of bf16 gradients go through the tensor cores: with ones in one row of A, a
+// product adds the values of 8 channels (lanes) for 4 state groups; its 10-bit
+// mantissa loses an eighth of what the bf16 gradient's own rounding does, and
+// the sums stay fp32 (8 products for two tokens against 58 exchanges, adds
+// and selects).  fp32 gradients are exchanged between lanes.
+template <typename IO, int L, bool VEC>
+__global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
+    ssm_bwd_kernel(SsmBwdArgs b, BwdParts part) {
+  using Shared = BwdShared<L>;
+  constexpr int CH = Shared::CH, SW = Shared::SW, kTile = Shared::TILE, K = kSsmChunk;
+  constexpr int WARPS = Shared::WARPS, PARTS = Shared::PARTS, CHUNKS = kTile / K;
+  constexpr int E = kTile * CH / kHelpers;   // (token, channel) pairs a helper
+  constexpr int BN = kTile * SW / kHelpers;  // values of B (and of C) a helper
+  constexpr int TPT = kHelpers / kTile;      // helpers a token (VEC)
+  constexpr int TSTEP = kHelpers / CH;       // tokens between two of a helper's (not VEC)
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(s_raw);
   const SsmArgs& a = b.f;
-  __shared__ float2 s_dt[K][CH];
-  __shared__ float s_dy[K][CH], s_fed[K][CH], s_qa[K][CH];
-  __shared__ __align__(16) float s_b[K][SW], s_c[K][SW];
-  __shared__ float s_part[WARPS][K][2][SW];
-  const int tid = threadIdx.x, l = tid % L, ch = tid / L, warp = tid / 32;
+  const int tid = threadIdx.x;
   const int n_blk = ssm_blocks(a, CH);
   const int seq = blockIdx.x / n_blk, block = blockIdx.x % n_blk;
   const SsmBlock blk(a, CH, block);
   int start, end;
   seq_range(a.cu, seq, a.T, &start, &end);
+  const int tiles = (end - start + kTile - 1) / kTile;
+  auto slot = [](int t, int c) {  // see the forward kernel
+    if (L != 4) return c;
+    const int p = c >> 1, o = p >> 2;
+    return ((o << 2 | ((p ^ o ^ t) & 1) | ((p ^ o) & 2)) << 1) | (c & 1);
+  };
 
-  const IO* u = static_cast<const IO*>(a.u);
-  const IO* delta = static_cast<const IO*>(a.delta);
-  const IO* z = static_cast<const IO*>(a.z);
-  const IO* dout = static_cast<const IO*>(b.d_out);
-  const IO* B = static_cast<const IO*>(a.B) + (int64_t)blk.g * a.b_group;
-  const IO* C = static_cast<const IO*>(a.C) + (int64_t)blk.g * a.c_group;
-  const bool on = ch < blk.n;
-  const int d = blk.c0 + (on ? ch : 0);
-  float A2[kSsmStates], dh[kSsmStates], dA[kSsmStates];
+  if (tid >= kSsmThreads) {
+    const int hid = tid - kSsmThreads;
+    const IO* u = static_cast<const IO*>(a.u) + blk.c0;
+    const IO* delta = static_cast<const IO*>(a.delta) + blk.c0;
+    const IO* z = a.z ? static_cast<const IO*>(a.z) + blk.c0 : nullptr;
+    const IO* dout = static_cast<const IO*>(b.d_out) + blk.c0;
+    const IO* B = static_cast<const IO*>(a.B) + (int64_t)blk.g * a.b_group;
+    const IO* C = static_cast<const IO*>(a.C) + (int64_t)blk.g * a.c_group;
+    IO* du = static_cast<IO*>(b.du) + blk.c0;
+    IO* ddelta = static_cast<IO*>(b.ddelta) + blk.c0;
+    const bool bc_vec = a.S % BN == 0 && a.b_stride % BN == 0 && a.c_stride % BN == 0 &&
+                        a.b_group % BN == 0 && a.c_group % BN == 0 &&
+                        (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C)) %
+                                Held<IO, BN, true>::ALIGN == 0;
+    auto tok_of = [&](int j) { return VEC ? hid / TPT : (j * kHelpers + hid) / CH; };
+    auto ch_of = [&](int j) { return VEC ? hid % TPT * E + j : (j * kHelpers + hid) % CH; };
+    const int bt = hid / TPT, bn = hid % TPT * BN;
+    constexpr int EC = VEC ? E : 1;  // channels a helper finishes
+    float bias[EC], skip[EC], dskip[EC], dbias[EC];
 #pragma unroll
-  for (int i = 0; i < kSsmStates; ++i) {
-    const int n = l * kSsmStates + i;
-    const bool real = on && n < a.S;
-    A2[i] = real ? a.A[(int64_t)d * a.S + n] * kLog2e : 0.f;
-    dh[i] = real && b.d_final ? b.d_final[((int64_t)seq * a.D + d) * a.S + n] : 0.f;
-    dA[i] = 0.f;
-  }
-  // the channel this thread finishes tokens of
-  const int oc = tid % CH;
-  const bool out_on = oc < blk.n;
-  const int od = blk.c0 + (out_on ? oc : 0);
-  const float bias = a.bias ? a.bias[od] : 0.f, skip = a.skip ? a.skip[od] : 0.f;
-  float dskip = 0.f, dbias = 0.f;
-
-  const int chunks = (end - start + K - 1) / K;
-  for (int k = chunks - 1; k >= 0; --k) {
-    const int t0 = start + k * K, m = min(K, end - t0);
-    for (int i = tid; i < K * CH; i += kSsmThreads) {
-      const int t = i / CH;
-      float2 v = make_float2(0.f, 0.f);
-      float dy = 0.f;
-      if (t < m && out_on) {
-        const int64_t tok = t0 + t;
-        const float raw = to_f32(delta[tok * a.delta_stride + od]) + bias;
-        v.x = a.softplus ? softplus_f(raw) : raw;
-        v.y = v.x * to_f32(u[tok * a.u_stride + od]);
-        dy = to_f32(dout[tok * a.D + od]);
+    for (int j = 0; j < EC; ++j) {
+      const int c = ch_of(j);
+      bias[j] = a.bias && c < blk.n ? a.bias[blk.c0 + c] : 0.f;
+      skip[j] = a.skip && c < blk.n ? a.skip[blk.c0 + c] : 0.f;
+      dskip[j] = dbias[j] = 0.f;
+    }
+    constexpr bool ONE = sizeof(IO) == 4;
+    struct Keep {  // what finish() needs of a tile
+      Held<IO, E, VEC> u, d;
+    } keep[2];
+    Held<IO, E, VEC> ru, rd, rz, ro;
+    Held<IO, BN, true> rb, rc;   // bc_vec, and fp32 either way
+    Held<IO, BN, false> sb, sc;  // bf16 otherwise
+    auto load_e = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, E, VEC>& r) {
+      r.clear();
+      if (VEC) {
+        if (tok_of(0) < m && ch_of(0) < blk.n)
+          r.all(p + (t0 + tok_of(0)) * stride + ch_of(0));
+      } else {
+        const IO* q = p + (t0 + tok_of(0)) * stride + ch_of(0);
+        const int left = ch_of(0) < blk.n ? m - tok_of(0) : 0;
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (j * TSTEP < left) r.one(j, q + j * (TSTEP * stride));
+      }
+    };
+    auto load_bc = [&](const IO* p, int64_t stride, int t0, int m, Held<IO, BN, true>& r,
+                       Held<IO, BN, false>& s) {
+      const IO* q = p + (int64_t)(t0 + bt) * stride + bn;
+      if (bc_vec) {
+        r.clear();
+        if (bt < m && bn < a.S) r.all(q);
+      } else {
+        if (ONE)
+          r.clear();
+        else
+          s.clear();
+#pragma unroll
+        for (int j = 0; j < BN; ++j)
+          if (bt < m && bn + j < a.S) {
+            if (ONE)
+              r.one(j, q + j);
+            else
+              s.one(j, q + j);
+          }
+      }
+    };
+    auto load = [&](int i) {
+      const int t0 = start + i * kTile, m = min(kTile, end - t0);
+      load_e(delta, a.delta_stride, t0, m, rd);
+      load_e(u, a.u_stride, t0, m, ru);
+      load_e(dout, a.D, t0, m, ro);
+      if (z) load_e(z, a.z_stride, t0, m, rz);
+      load_bc(B, a.b_stride, t0, m, rb, sb);
+      load_bc(C, a.c_stride, t0, m, rc, sc);
+    };
+    auto convert = [&](int i, int w, Keep& k) {
+      const int t0 = start + i * kTile, m = min(kTile, end - t0);
+      float dt[E], dtu[E], dy[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float raw = rd.get(j) + bias[VEC ? j : 0];
+        const bool real = tok_of(j) < m && ch_of(j) < blk.n;
+        dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
+        dtu[j] = dt[j] * ru.get(j);
+        dy[j] = ro.get(j);
         if (z) {
-          const float g = to_f32(z[tok * a.z_stride + od]);
-          dy *= g * sigmoid_f(g);
+          const float g = rz.get(j);
+          dy[j] *= g * sigmoid_f(g);
         }
       }
-      s_dt[t][oc] = v;
-      s_dy[t][oc] = dy;
-    }
-    for (int i = tid; i < K * SW; i += kSsmThreads) {
-      const int t = i / SW, n = i % SW;
-      const bool real = t < m && n < a.S;
-      s_b[t][n] = real ? to_f32(B[(int64_t)(t0 + t) * a.b_stride + n]) : 0.f;
-      s_c[t][n] = real ? to_f32(C[(int64_t)(t0 + t) * a.c_stride + n]) : 0.f;
-    }
-    float hp[K + 1][kSsmStates], av[K][kSsmStates];
-    const float* hs = part.states + (ssm_piece_id(seq, start, K, k) * a.D + d) * a.S;
+      k.u = ru;
+      k.d = rd;
+      if (VEC && E >= 2) {
 #pragma unroll
-    for (int i = 0; i < kSsmStates; ++i)
-      hp[0][i] = on && l * kSsmStates + i < a.S ? hs[l * kSsmStates + i] : 0.f;
+        for (int j = 0; j < E; j += 2)
+          *reinterpret_cast<float4*>(&sh.dt[w][tok_of(0)][slot(tok_of(0), ch_of(j))]) =
+              make_float4(dt[j], dtu[j], dt[j + 1], dtu[j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          sh.dt[w][tok_of(j)][slot(tok_of(j), ch_of(j))] = make_float2(dt[j], dtu[j]);
+      }
+      if (VEC) {
+        store_floats<E>(&sh.dy[w][tok_of(0)][ch_of(0)], dy);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) sh.dy[w][tok_of(j)][ch_of(j)] = dy[j];
+      }
+      float vb[BN], vc[BN];
+#pragma unroll
+      for (int j = 0; j < BN; ++j) {
+        vb[j] = ONE || bc_vec ? rb.get(j) : sb.get(j);
+        vc[j] = ONE || bc_vec ? rc.get(j) : sc.get(j);
+      }
+      store_floats<BN>(&sh.b[w][bt][bn], vb);
+      store_floats<BN>(&sh.c[w][bt][bn], vc);
+    };
+    // reads only this thread's own elements of dt and dy, before convert()
+    // writes them again
+    auto finish = [&](int i, int w, const Keep& k) {
+      const int t0 = start + i * kTile, m = min(kTile, end - t0);
+      float ru_[E], rd_[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int t = tok_of(j), c = ch_of(j);
+        const float uu = k.u.get(j), raw = k.d.get(j) + bias[VEC ? j : 0];
+        const float f = sh.fed[w][t][c], dy = sh.dy[w][t][c];
+        float dd = fmaf(f, uu, kLn2 * sh.qa[w][t][c]);
+        if (a.softplus) dd *= sigmoid_f(raw);
+        if (t < m && c < blk.n) {
+          dskip[VEC ? j : 0] = fmaf(dy, uu, dskip[VEC ? j : 0]);
+          dbias[VEC ? j : 0] += dd;
+        }
+        ru_[j] = fmaf(f, sh.dt[w][t][slot(t, c)].x, dy * skip[VEC ? j : 0]);
+        rd_[j] = dd;
+      }
+      if (VEC) {
+        if (tok_of(0) < m && ch_of(0) < blk.n) {
+          const int64_t at = (int64_t)(t0 + tok_of(0)) * a.D + ch_of(0);
+          store_vec<IO, E>(du + at, ru_);
+          store_vec<IO, E>(ddelta + at, rd_);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (tok_of(j) < m && ch_of(j) < blk.n) {
+            const int64_t at = (int64_t)(t0 + tok_of(j)) * a.D + ch_of(j);
+            du[at] = from_f32<IO>(ru_[j]);
+            ddelta[at] = from_f32<IO>(rd_[j]);
+          }
+      }
+      // the warps' dB and dC
+      float* to = part.bc + ((int64_t)block * a.tokens + t0) * 2 * a.S;
+      if (a.S == SW) {
+        for (int e = hid * 4; e < m * 2 * SW; e += kHelpers * 4) {
+          float4 s = *reinterpret_cast<const float4*>(&sh.part[w % PARTS][0][0][0][0] + e);
+#pragma unroll
+          for (int q = 1; q < WARPS; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(&sh.part[w % PARTS][q][0][0][0] + e);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+          }
+          *reinterpret_cast<float4*>(to + e) = s;
+        }
+      } else {
+        for (int e = hid; e < m * 2 * SW; e += kHelpers) {
+          const int n = e % SW;
+          if (n >= a.S) continue;
+          float s = 0.f;
+#pragma unroll
+          for (int q = 0; q < WARPS; ++q) s += (&sh.part[w % PARTS][q][0][0][0])[e];
+          to[e / SW * a.S + n] = s;
+        }
+      }
+    };
+    if (tiles > 0) {
+      load(tiles - 1);
+      convert(tiles - 1, 0, keep[0]);
+      if (tiles > 1) load(tiles - 2);
+    }
     __syncthreads();
+    for (int n = 0; n < tiles; n += 2) {  // tile tiles - 1 - n - k in buffer k
 #pragma unroll
-    for (int t = 0; t < K; ++t) {
-      const float2 v = s_dt[t][ch];
-      const float4 bv = *reinterpret_cast<const float4*>(&s_b[t][l * kSsmStates]);
-      const float bb[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-      for (int i = 0; i < kSsmStates; ++i) {
-        av[t][i] = ex2_f(v.x * A2[i]);
-        hp[t + 1][i] = fmaf(av[t][i], hp[t][i], v.y * bb[i]);
+      for (int k = 0; k < 2; ++k) {
+        const int i = tiles - 1 - n - k;
+        if (i < 0) break;
+        if (n + k > 0) finish(i + 1, 1 - k, keep[1 - k]);
+        if (PARTS == 1) __syncthreads();
+        if (i > 0) {
+          convert(i - 1, 1 - k, keep[1 - k]);
+          if (i > 1) load(i - 2);
+        }
+        __syncthreads();
       }
     }
-    float fed[K], qa[K], dAc[kSsmStates] = {};
+    if (tiles > 0) {
+      if (tiles & 1)
+        finish(0, 0, keep[0]);
+      else
+        finish(0, 1, keep[1]);
+    }
+    // sums over the helpers of one channel, in the order of the helpers
+    float* s_sum = &sh.dt[0][0][0].x;  // [2][kHelpers][EC]
+    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers));
 #pragma unroll
-    for (int t = K - 1; t >= 0; --t) {
-      const float2 v = s_dt[t][ch];
-      const float dy = s_dy[t][ch];
-      const float4 bv = *reinterpret_cast<const float4*>(&s_b[t][l * kSsmStates]);
-      const float4 cv = *reinterpret_cast<const float4*>(&s_c[t][l * kSsmStates]);
-      const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
-      float bc[2 * kSsmStates];
-      fed[t] = 0.f;
-      qa[t] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kSsmStates; ++i) {
-        dh[i] = fmaf(dy, cc[i], dh[i]);
-        bc[i] = dh[i] * v.y;
-        bc[kSsmStates + i] = dy * hp[t + 1][i];
-        fed[t] = fmaf(dh[i], bb[i], fed[t]);
-        dh[i] *= av[t][i];
-        const float q = dh[i] * hp[t][i];
-        qa[t] = fmaf(q, A2[i], qa[t]);
-        dAc[i] = fmaf(q, v.x, dAc[i]);
+    for (int j = 0; j < EC; ++j) {
+      s_sum[hid * EC + j] = dskip[j];
+      s_sum[(kHelpers + hid) * EC + j] = dbias[j];
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers));
+    for (int c = hid; c < blk.n; c += kHelpers) {
+      float x = 0.f, y = 0.f;
+      const int first = VEC ? c / E : c, step = VEC ? TPT : CH, j = VEC ? c % E : 0;
+      for (int h = first; h < kHelpers; h += step) {
+        x += s_sum[h * EC + j];
+        y += s_sum[(kHelpers + h) * EC + j];
       }
-      int first = 0;
-      SpreadSum<2 * kSsmStates, L, 32>::run(bc, tid, first);
-      constexpr int LEFT = 2 * kSsmStates / (32 / L) > 1 ? 2 * kSsmStates / (32 / L) : 1;
-#pragma unroll
-      for (int i = 0; i < LEFT; ++i) {
-        const int e = first + i;
-        s_part[warp][t][e / kSsmStates][l * kSsmStates + e % kSsmStates] = bc[i];
-      }
+      part.dskip[(int64_t)seq * a.D + blk.c0 + c] = x;
+      part.dbias[(int64_t)seq * a.D + blk.c0 + c] = y;
     }
-#pragma unroll
-    for (int i = 0; i < kSsmStates; ++i) dA[i] += dAc[i];
-    int first = 0, first2 = 0;
-    SpreadSum<K, 1, L>::run(fed, l, first);
-    SpreadSum<K, 1, L>::run(qa, l, first2);
-    constexpr int LEFT = K / L > 1 ? K / L : 1;
-#pragma unroll
-    for (int i = 0; i < LEFT; ++i) {
-      s_fed[first + i][ch] = fed[i];
-      s_qa[first + i][ch] = qa[i];
-    }
-    __syncthreads();
-    for (int i = tid; i < m * CH; i += kSsmThreads) {
-      const int t = i / CH;
-      if (!out_on) continue;
-      const int64_t tok = t0 + t;
-      const float raw = to_f32(delta[tok * a.delta_stride + od]) + bias;
-      const float uu = to_f32(u[tok * a.u_stride + od]);
-      const float dy = s_dy[t][oc], f = s_fed[t][oc];
-      float dd = fmaf(f, uu, kLn2 * s_qa[t][oc]);
-      if (a.softplus) dd *= sigmoid_f(raw);
-      dskip = fmaf(dy, uu, dskip);
-      dbias += dd;
-      static_cast<IO*>(b.du)[tok * a.D + od] = from_f32<IO>(fmaf(f, s_dt[t][oc].x, dy * skip));
-      static_cast<IO*>(b.ddelta)[tok * a.D + od] = from_f32<IO>(dd);
-    }
-    for (int i = tid; i < m * 2 * SW; i += kSsmThreads) {
-      const int t = i / (2 * SW), which = i / SW % 2, n = i % SW;
-      if (n >= a.S) continue;
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) s += s_part[w][t][which][n];
-      part.bc[(((int64_t)block * a.tokens + t0 + t) * 2 + which) * a.S + n] = s;
-    }
-    __syncthreads();
+    return;
   }
+
+  constexpr int CW = 32 / L;  // channels a warp, in the low lane bits
+  constexpr bool TENSOR = L == 4 && sizeof(IO) == 2;
+  const int warp = tid / 32, lane = tid % 32, l = lane / CW, ch = warp * CW + lane % CW;
+  const bool on = ch < blk.n;
+  const int d = blk.c0 + (on ? ch : 0), n0 = l * kSsmStates;
+  const int slot0 = slot(0, ch), slot1 = slot(1, ch);
+  const bool st_vec = a.S % 4 == 0;
+  float A2[kSsmStates], g0[kSsmStates];
 #pragma unroll
   for (int i = 0; i < kSsmStates; ++i) {
-    const int n = l * kSsmStates + i;
-    if (!on || n >= a.S) continue;
-    const int64_t at = ((int64_t)seq * a.D + d) * a.S + n;
-    part.dA[at] = dA[i];
-    if (b.dh0) b.dh0[at] = dh[i];
+    const bool real = on && n0 + i < a.S;
+    A2[i] = real ? a.A[(int64_t)d * a.S + n0 + i] * kLog2e : 0.f;
+    g0[i] = real && b.d_final ? b.d_final[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
   }
-  // sums over the threads that finished tokens of one channel
-  float* sum = &s_part[0][0][0][0];
-  sum[tid] = dskip;
-  sum[kSsmThreads + tid] = dbias;
+  const f32x2 A01 = pack2(A2[0], A2[1]), A23 = pack2(A2[2], A2[3]);
+  f32x2 dh01 = pack2(g0[0], g0[1]), dh23 = pack2(g0[2], g0[3]);
+  f32x2 dA01 = both(0.f), dA23 = both(0.f);
+  auto fetch = [&](int i, int w) {  // the start states of tile i's chunks
+    if (!st_vec || !on || n0 >= a.S) return;
+    const int t0 = i * kTile, m = min(kTile, end - start - t0);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+      if (c * K < m) {
+        const float* p = part.states +
+                         (ssm_piece_id(seq, start, K, t0 / K + c) * a.D + d) * a.S + n0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::
+                     "r"((unsigned)__cvta_generic_to_shared(&sh.state[w][c][tid])), "l"(p));
+      }
+  };
+  if (tiles > 0) fetch(tiles - 1, 0);
+  asm volatile("cp.async.commit_group;");
   __syncthreads();
-  if (tid < CH && tid < blk.n) {
-    float x = 0.f, y = 0.f;
-    for (int i = tid; i < kSsmThreads; i += CH) {
-      x += sum[i];
-      y += sum[kSsmThreads + i];
+  for (int n = 0; n < tiles; ++n) {
+    const int i = tiles - 1 - n, w = n & 1, m = min(kTile, end - start - i * kTile);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (i > 0) fetch(i - 1, w ^ 1);
+    asm volatile("cp.async.commit_group;");
+    if (PARTS == 1) __syncthreads();
+    for (int c = (m - 1) / K; c >= 0; --c) {
+      const int tc = c * K;
+      f32x2 h01[K + 1], h23[K + 1], e01[K], e23[K];
+      if (st_vec) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on && n0 < a.S) v = sh.state[w][c][tid];
+        h01[0] = pack2(v.x, v.y);
+        h23[0] = pack2(v.z, v.w);
+      } else {
+        const float* p =
+            part.states + (ssm_piece_id(seq, start, K, i * CHUNKS + c) * a.D + d) * a.S + n0;
+        float v[kSsmStates];
+#pragma unroll
+        for (int k = 0; k < kSsmStates; ++k) v[k] = on && n0 + k < a.S ? p[k] : 0.f;
+        h01[0] = pack2(v[0], v[1]);
+        h23[0] = pack2(v[2], v[3]);
+      }
+#pragma unroll
+      for (int t = 0; t < K; ++t) {
+        const float2 v = sh.dt[w][tc + t][t & 1 ? slot1 : slot0];
+        const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.b[w][tc + t][n0]);
+        const f32x2 dt = both(v.x), dtu = both(v.y);
+        float p[4];
+        unpack2(mul2(dt, A01), p[0], p[1]);
+        unpack2(mul2(dt, A23), p[2], p[3]);
+        e01[t] = pack2(ex2_f(p[0]), ex2_f(p[1]));
+        e23[t] = pack2(ex2_f(p[2]), ex2_f(p[3]));
+        h01[t + 1] = fma2(e01[t], h01[t], mul2(dtu, bv.x));
+        h23[t + 1] = fma2(e23[t], h23[t], mul2(dtu, bv.y));
+      }
+      f32x2 s01 = both(0.f), s23 = both(0.f);  // dA of the chunk
+      float fed[4], qa[4], sums[4];
+#pragma unroll
+      for (int t = K - 1; t >= 0; --t) {
+        const float2 v = sh.dt[w][tc + t][t & 1 ? slot1 : slot0];
+        const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.b[w][tc + t][n0]);
+        const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sh.c[w][tc + t][n0]);
+        const f32x2 dy = both(sh.dy[w][tc + t][ch]), dt = both(v.x), dtu = both(v.y);
+        dh01 = fma2(dy, cv.x, dh01);
+        dh23 = fma2(dy, cv.y, dh23);
+        float bc[8];
+        unpack2(mul2(dh01, dtu), bc[0], bc[1]);
+        unpack2(mul2(dh23, dtu), bc[2], bc[3]);
+        unpack2(mul2(dy, h01[t + 1]), bc[4], bc[5]);
+        unpack2(mul2(dy, h23[t + 1]), bc[6], bc[7]);
+        fed[t & 3] = sum2(fma2(dh01, bv.x, mul2(dh23, bv.y)));
+        dh01 = mul2(dh01, e01[t]);
+        dh23 = mul2(dh23, e23[t]);
+        const f32x2 q01 = mul2(dh01, h01[t]), q23 = mul2(dh23, h23[t]);
+        qa[t & 3] = sum2(fma2(q01, A01, mul2(q23, A23)));
+        s01 = fma2(q01, dt, s01);
+        s23 = fma2(q23, dt, s23);
+        if constexpr (TENSOR) {
+          // tokens t (odd) and t - 1: product 4 (t & 1) + j adds dB_j into row
+          // 4 (t & 1) + j and dC_j into the row 8 below, for the state groups
+          // and the channels' two halves as columns
+          if (t & 1) sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t one = lane / 4 == (t & 1) * 4 + j ? 0x3f800000u : 0u;
+            mma_tf32(sums, one, 0u, 0u, one, bc[j], bc[4 + j]);
+          }
+          if (!(t & 1)) {
+            const int q = lane / 4, at = lane % 4 * 4 + (q & 3);
+            sh.part[w % PARTS][warp][tc + t + q / 4][0][at] = sums[0] + sums[1];
+            sh.part[w % PARTS][warp][tc + t + q / 4][1][at] = sums[2] + sums[3];
+          }
+        } else {
+          int f = 0;
+          SpreadSum<8, 1, CW>::run(bc, lane, f);
+          constexpr int LEFT = 8 / CW > 1 ? 8 / CW : 1;
+#pragma unroll
+          for (int k = 0; k < LEFT; ++k)
+            sh.part[w % PARTS][warp][tc + t][(f + k) / 4][n0 + (f + k) % 4] = bc[k];
+        }
+        if ((t & 3) == 0) {  // four tokens' sums over the state groups
+          int f = 0, f2 = 0;
+          SpreadSum<4, CW, 32>::run(fed, lane, f);
+          SpreadSum<4, CW, 32>::run(qa, lane, f2);
+          constexpr int LEFT = L >= 4 ? 1 : 4 / L;
+          if (l < 4)
+#pragma unroll
+            for (int k = 0; k < LEFT; ++k) {
+              sh.fed[w][tc + t + f + k][ch] = fed[k];
+              sh.qa[w][tc + t + f + k][ch] = qa[k];
+            }
+        }
+      }
+      dA01 = add2(dA01, s01);
+      dA23 = add2(dA23, s23);
     }
-    part.dskip[(int64_t)seq * a.D + blk.c0 + tid] = x;
-    part.dbias[(int64_t)seq * a.D + blk.c0 + tid] = y;
+    __syncthreads();
+  }
+  float dA[kSsmStates], dh[kSsmStates];
+  unpack2(dA01, dA[0], dA[1]);
+  unpack2(dA23, dA[2], dA[3]);
+  unpack2(dh01, dh[0], dh[1]);
+  unpack2(dh23, dh[2], dh[3]);
+#pragma unroll
+  for (int k = 0; k < kSsmStates; ++k) {
+    if (!on || n0 + k >= a.S) continue;
+    const int64_t at = ((int64_t)seq * a.D + d) * a.S + n0 + k;
+    part.dA[at] = dA[k];
+    if (b.dh0) b.dh0[at] = dh[k];
   }
 }
 
@@ -253,10 +515,27 @@ Layout layout(const SsmBwdArgs& b) {
   return o;
 }
 
+template <typename IO, int E>
+bool vec_ok(const SsmBwdArgs& b) {
+  const SsmArgs& a = b.f;
+  const void* ps[] = {a.u, a.delta, a.z, b.d_out, b.du, b.ddelta};
+  for (const void* p : ps)
+    if (p && !aligned_to(p, Held<IO, E, true>::ALIGN)) return false;
+  return a.D / a.G % E == 0 && a.D % E == 0 && a.u_stride % E == 0 && a.delta_stride % E == 0 &&
+         a.z_stride % E == 0;
+}
+
 template <typename IO, int L>
 cudaError_t bwd_launch(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st) {
   const unsigned grid = (unsigned)ssm_blocks(b.f, kSsmThreads / L) * (unsigned)b.f.n_seqs;
-  if (grid) ssm_bwd_kernel<IO, L><<<grid, kSsmThreads, 0, st>>>(b, part);
+  if (!grid) return cudaSuccess;
+  constexpr int E = tile_of(L) * (kSsmThreads / L) / kHelpers;
+  auto* k = vec_ok<IO, E>(b) ? ssm_bwd_kernel<IO, L, true> : ssm_bwd_kernel<IO, L, false>;
+  constexpr int bytes = sizeof(BwdShared<L>);
+  static_assert(bytes <= 227 * 1024, "shared memory of an SM");
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  k<<<grid, kSsmThreads + kHelpers, bytes, st>>>(b, part);
   return cudaGetLastError();
 }
 

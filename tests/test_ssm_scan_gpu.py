@@ -249,9 +249,16 @@ def test_misaligned_slices_match_aligned():
     for x, y in zip(K.ssm_scan_fwd(*a, z=d["z"], **kw),
                     K.ssm_scan_fwd(*b, z=off(d["z"], 1), **kw)):
         assert torch.equal(x, y)
-    for x, y in zip(K.ssm_scan_bwd(*a, z=d["z"], d_out=d["d_out"], **kw),
-                    K.ssm_scan_bwd(*b, z=off(d["z"], 1), d_out=d["d_out"], **kw)):
-        assert torch.equal(x, y)
+    for name, x, y in zip(
+            NAMES, K.ssm_scan_bwd(*a, z=d["z"], d_out=d["d_out"], **kw),
+            K.ssm_scan_bwd(*b, z=off(d["z"], 1), d_out=d["d_out"], **kw)):
+        if name in ("D", "delta_bias"):
+            # single loads give a thread other tokens of a channel, so these
+            # sums over 100 tokens are added in another order: each of 100
+            # partial sums rounds by 2^-24 of at most the sum of the terms
+            R.check("d " + name, y, x.cpu().double(), 100 * 2.0 ** -24)
+        else:
+            assert torch.equal(x, y), name
 
 
 def test_non_finite_inputs_stay_in_their_channel():
