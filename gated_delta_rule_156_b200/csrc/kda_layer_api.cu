@@ -364,8 +364,9 @@ kda_status kda_ssm_scan_bwd(const kda_ssm_shape* shape, const void* u, const voi
                        flat(d_skip, a.D, 4), flat(dz, a.tokens * a.D, e),
                        flat(d_delta_bias, a.D, 4), flat(d_initial_state, state, 4)};
   if ((st = check_memory(in, 12, outs, 9)) != KDA_OK) return st;
-  return with_workspace(kda::ssm_bwd_workspace_bytes(b), stream,
-                        [&](void* ws) { return kda::launch_ssm_bwd(b, ws, stream); });
+  const int sms = kda::sm_count();
+  return with_workspace(kda::ssm_bwd_workspace_bytes(b, sms), stream,
+                        [&](void* ws) { return kda::launch_ssm_bwd(b, ws, sms, stream); });
 }
 
 kda_status kda_ssm_scan_bwd_plan(const kda_ssm_shape* shape, int packed, int* kernels,
@@ -373,10 +374,11 @@ kda_status kda_ssm_scan_bwd_plan(const kda_ssm_shape* shape, int packed, int* ke
   kda::SsmBwdArgs b{};
   const kda_status st = ssm_bwd_args(shape, packed != 0, &b);
   if (st != KDA_OK) return st;
-  static float tag;  // as a call that asks for every gradient
-  b.dskip = b.dbias = &tag;
-  if (kernels) *kernels = kda::ssm_bwd_kernel_count(b);
-  if (workspace_bytes) *workspace_bytes = kda::ssm_bwd_workspace_bytes(b);
+  static const int32_t tag = 0;  // only tells the planner the layout
+  b.f.cu = packed ? &tag : nullptr;
+  const int sms = kda::sm_count();
+  if (kernels) *kernels = kda::ssm_bwd_kernel_count(b, sms);
+  if (workspace_bytes) *workspace_bytes = kda::ssm_bwd_workspace_bytes(b, sms);
   return KDA_OK;
 }
 

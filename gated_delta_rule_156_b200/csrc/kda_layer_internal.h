@@ -73,9 +73,9 @@ struct SsmBwdArgs {
   void *du, *ddelta, *dB, *dC, *dz;
   float *dA, *dskip, *dbias, *dh0;
 };
-size_t ssm_bwd_workspace_bytes(const SsmBwdArgs& a);
-int ssm_bwd_kernel_count(const SsmBwdArgs& a);
-cudaError_t launch_ssm_bwd(const SsmBwdArgs& a, void* workspace, cudaStream_t stream);
+size_t ssm_bwd_workspace_bytes(const SsmBwdArgs& a, int sms);
+int ssm_bwd_kernel_count(const SsmBwdArgs& a, int sms);
+cudaError_t launch_ssm_bwd(const SsmBwdArgs& a, void* workspace, int sms, cudaStream_t stream);
 
 struct NormArgs {
   const void *x, *gate, *residual;               // gate, residual may be null

@@ -468,12 +468,10 @@ bool vec_ok(const SsmArgs& a, const SsmSave& save) {
          a.z_stride % E == 0;
 }
 
-int64_t segments(const SsmArgs& a, int seg) { return a.tokens / seg + a.n_seqs + 1; }
-
 template <typename IO, int L, int MODE>
 cudaError_t fwd_launch(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,
                        cudaStream_t st) {
-  const int64_t ids = split.seg == INT32_MAX ? a.n_seqs : segments(a, split.seg);
+  const int64_t ids = split.seg == INT32_MAX ? a.n_seqs : ssm_segments(a, split.seg);
   const unsigned grid = (unsigned)(ids * ssm_blocks(a, kSsmThreads / L));
   constexpr int E = tile_of(L) * (kSsmThreads / L) / kHelpers;
   auto* k = vec_ok<IO, E>(a, save) ? ssm_fwd_kernel<IO, L, MODE, true>
@@ -535,26 +533,26 @@ cudaError_t step_pick(const SsmArgs& a, cudaStream_t st) {
 // Splitting costs a second pass over the recurrence (without its outputs), so
 // it pays where the sequences' own CTAs leave most of the SMs idle: a segment
 // is what each of the SMs' CTA slots (two an SM) would get of the whole, and
-// sequences are cut where they hold three of them.  One sequence of 4096 tokens
+// sequences are cut where they hold `least` of them, three for the forward.  One sequence of 4096 tokens
 // whole and split: 159 and 27 us with 256 channels, 161 and 122 us with 2048;
 // with 4096 channels, 2.3 segments, 198 and 230 us.  Packed lengths are not
 // known on the host; their longest is taken to be 2.5 times the mean.
-int ssm_segment(const SsmArgs& a, int sms) {
+int ssm_segment(const SsmArgs& a, int sms, double least) {
   if (a.n_seqs < 1) return INT32_MAX;
   const int64_t blocks = ssm_blocks(a, kSsmThreads / ssm_lanes(a.S)), slots = 2 * (int64_t)sms;
   int64_t seg = (a.tokens * blocks + slots - 1) / slots;
   seg = seg < kMinSegment ? kMinSegment : (seg + 31) / 32 * 32;
   const double longest = (double)a.tokens / a.n_seqs * (a.cu && a.n_seqs > 1 ? 2.5 : 1.0);
-  return longest >= 3.0 * seg ? (int)seg : INT32_MAX;
+  return longest >= least * seg ? (int)seg : INT32_MAX;
 }
 
 size_t ssm_split_bytes(const SsmArgs& a, int seg) {
-  return seg == INT32_MAX ? 0 : (size_t)segments(a, seg) * a.D * (a.S + 1) * sizeof(float);
+  return seg == INT32_MAX ? 0 : (size_t)ssm_segments(a, seg) * a.D * (a.S + 1) * sizeof(float);
 }
 
 SsmSplit ssm_split_at(const SsmArgs& a, int seg, void* workspace) {
   SsmSplit s{seg, static_cast<float*>(workspace), nullptr};
-  if (seg != INT32_MAX) s.steps = s.ends + segments(a, seg) * a.D * a.S;
+  if (seg != INT32_MAX) s.steps = s.ends + ssm_segments(a, seg) * a.D * a.S;
   return s;
 }
 
@@ -575,12 +573,12 @@ cudaError_t scan(const SsmArgs& a, const SsmSave* save, const SsmSplit& split, c
 }  // namespace
 
 size_t ssm_fwd_workspace_bytes(const SsmArgs& a, int sms) {
-  return ssm_split_bytes(a, ssm_segment(a, sms));
+  return ssm_split_bytes(a, ssm_segment(a, sms, 3.0));
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, void* workspace, int sms, cudaStream_t st) {
   if (a.n_seqs == 0) return cudaSuccess;
-  const SsmSplit split = ssm_split_at(a, ssm_segment(a, sms), workspace);
+  const SsmSplit split = ssm_split_at(a, ssm_segment(a, sms, 3.0), workspace);
   return a.bf16 ? scan<__nv_bfloat16>(a, nullptr, split, st) : scan<float>(a, nullptr, split, st);
 }
 

@@ -182,9 +182,11 @@ struct SsmSave {
   const void* d_out;  // for dz
   void* dz;
 };
-// Tokens per segment of a scan over `a` on a device of `sms` SMs, INT32_MAX
-// where it is not split, and the workspace that a split takes.
-int ssm_segment(const SsmArgs& a, int sms);
+// Tokens per segment of a scan over `a` on a device of `sms` SMs where a
+// sequence makes `least` of them, else INT32_MAX (not split); an upper bound of
+// the segment ids, and the workspace that a split takes.
+int ssm_segment(const SsmArgs& a, int sms, double least);
+inline int64_t ssm_segments(const SsmArgs& a, int seg) { return a.tokens / seg + a.n_seqs + 1; }
 size_t ssm_split_bytes(const SsmArgs& a, int seg);
 SsmSplit ssm_split_at(const SsmArgs& a, int seg, void* workspace);
 cudaError_t launch_ssm_save(const SsmArgs& a, const SsmSave& save, const SsmSplit& split,

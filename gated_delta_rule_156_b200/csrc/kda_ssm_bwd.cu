@@ -21,23 +21,11 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdParts {
-  float* states;  // [piece ids of 8 tokens][D][S]
-  float* bc;      // [channel block][token][2][S]
-  float* dA;      // [n_seqs][D][S]
-  float* dskip;   // [n_seqs][D]
-  float* dbias;   // [n_seqs][D]
+  float* states;   // [piece ids of 8 tokens][D][S]
+  float* bc;       // [channel block][token][2][S]
+  float* small;    // [segment id][D (S + 2)]: dA, dskip, dbias of a segment
+  SsmSplit split;  // the segments; ends and steps of the backward's first pass
 };
-
-// D += A B of one warp, 16 x 8 by 8 x 8, in tf32 with fp32 sums.  The operands'
-// bits are used as they are: the tensor cores read the upper 10 bits of the
-// mantissa.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, float b0, float b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
-}
 
 template <int L>
 struct BwdShared {
@@ -62,13 +50,15 @@ struct BwdShared {
 // ahead.
 //
 // Per chunk of 8 tokens a thread runs its 4 states forward, keeping them and
-// their decays in registers, and then back.  The sums over channels (dB, dC)
-// of bf16 gradients go through the tensor cores: with ones in one row of A, a
-// product adds the values of 8 channels (lanes) for 4 state groups; its 10-bit
-// mantissa loses an eighth of what the bf16 gradient's own rounding does, and
-// the sums stay fp32 (8 products for two tokens against 58 exchanges, adds
-// and selects).  fp32 gradients are exchanged between lanes.
-template <typename IO, int L, bool VEC>
+// their decays in registers, and then back.  dB and dC are summed over the
+// warp's channels by exchanges: 8 values a token in 7 of them.  (Products with
+// a row of ones on the tensor cores, mma.sync in tf32, take fewer instructions
+// but were slower, 1.39 against 1.23 ms for 2 x 4096 tokens of 4096 channels,
+// and less exact.)  The kernel is bound by the issue of these instructions.
+//
+// ENDS: a split scan's first pass backward (see SsmSplit): each segment's
+// gradient into its start state from none at its end, and its sum of steps.
+template <typename IO, int L, bool VEC, bool ENDS>
 __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     ssm_bwd_kernel(SsmBwdArgs b, BwdParts part) {
   using Shared = BwdShared<L>;
@@ -82,11 +72,25 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   Shared& sh = *reinterpret_cast<Shared*>(s_raw);
   const SsmArgs& a = b.f;
   const int tid = threadIdx.x;
-  const int n_blk = ssm_blocks(a, CH);
-  const int seq = blockIdx.x / n_blk, block = blockIdx.x % n_blk;
+  const int n_blk = ssm_blocks(a, CH), block = blockIdx.x % n_blk;
+  const int64_t id = blockIdx.x / n_blk;
   const SsmBlock blk(a, CH, block);
-  int start, end;
-  seq_range(a.cu, seq, a.T, &start, &end);
+  float* small = part.small + id * a.D * (a.S + 2);  // of this segment
+  const SsmSplit& split = part.split;
+  const bool cut = split.seg != INT32_MAX;
+  int seq, piece, seq_start, seq_end;
+  if (!ssm_piece(a, split.seg, id, &seq, &piece, &seq_start, &seq_end)) {
+    if (!ENDS) {  // an id without a segment adds nothing to the sums
+      for (int i = tid; i < blk.n * a.S; i += kSsmThreads + kHelpers)
+        small[(int64_t)blk.c0 * a.S + i] = 0.f;
+      for (int i = tid; i < 2 * blk.n; i += kSsmThreads + kHelpers)
+        small[(int64_t)a.D * (a.S + i / blk.n) + blk.c0 + i % blk.n] = 0.f;
+    }
+    return;
+  }
+  if (ENDS && piece == 0) return;  // nothing lies before it
+  const int start = seq_start + piece * (cut ? split.seg : 0);
+  const int end = min(seq_end, (int)min((int64_t)start + split.seg, (int64_t)INT32_MAX));
   const int tiles = (end - start + kTile - 1) / kTile;
   auto slot = [](int t, int c) {  // see the forward kernel
     if (L != 4) return c;
@@ -164,10 +168,10 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     auto load = [&](int i) {
       const int t0 = start + i * kTile, m = min(kTile, end - t0);
       load_e(delta, a.delta_stride, t0, m, rd);
-      load_e(u, a.u_stride, t0, m, ru);
+      if (!ENDS) load_e(u, a.u_stride, t0, m, ru);
       load_e(dout, a.D, t0, m, ro);
       if (z) load_e(z, a.z_stride, t0, m, rz);
-      load_bc(B, a.b_stride, t0, m, rb, sb);
+      if (!ENDS) load_bc(B, a.b_stride, t0, m, rb, sb);
       load_bc(C, a.c_stride, t0, m, rc, sc);
     };
     auto convert = [&](int i, int w, Keep& k) {
@@ -178,15 +182,17 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         const float raw = rd.get(j) + bias[VEC ? j : 0];
         const bool real = tok_of(j) < m && ch_of(j) < blk.n;
         dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
-        dtu[j] = dt[j] * ru.get(j);
+        dtu[j] = ENDS ? 0.f : dt[j] * ru.get(j);
         dy[j] = ro.get(j);
         if (z) {
           const float g = rz.get(j);
           dy[j] *= g * sigmoid_f(g);
         }
       }
-      k.u = ru;
-      k.d = rd;
+      if (!ENDS) {
+        k.u = ru;
+        k.d = rd;
+      }
       if (VEC && E >= 2) {
 #pragma unroll
         for (int j = 0; j < E; j += 2)
@@ -206,10 +212,10 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       float vb[BN], vc[BN];
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
-        vb[j] = ONE || bc_vec ? rb.get(j) : sb.get(j);
+        if (!ENDS) vb[j] = ONE || bc_vec ? rb.get(j) : sb.get(j);
         vc[j] = ONE || bc_vec ? rc.get(j) : sc.get(j);
       }
-      store_floats<BN>(&sh.b[w][bt][bn], vb);
+      if (!ENDS) store_floats<BN>(&sh.b[w][bt][bn], vb);
       store_floats<BN>(&sh.c[w][bt][bn], vc);
     };
     // reads only this thread's own elements of dt and dy, before convert()
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       for (int k = 0; k < 2; ++k) {
         const int i = tiles - 1 - n - k;
         if (i < 0) break;
-        if (n + k > 0) finish(i + 1, 1 - k, keep[1 - k]);
+        if (!ENDS && n + k > 0) finish(i + 1, 1 - k, keep[1 - k]);
         if (PARTS == 1) __syncthreads();
         if (i > 0) {
           convert(i - 1, 1 - k, keep[1 - k]);
@@ -292,6 +298,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         __syncthreads();
       }
     }
+    if (ENDS) return;
     if (tiles > 0) {
       if (tiles & 1)
         finish(0, 0, keep[0]);
@@ -314,14 +321,13 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         x += s_sum[h * EC + j];
         y += s_sum[(kHelpers + h) * EC + j];
       }
-      part.dskip[(int64_t)seq * a.D + blk.c0 + c] = x;
-      part.dbias[(int64_t)seq * a.D + blk.c0 + c] = y;
+      small[(int64_t)a.D * a.S + blk.c0 + c] = x;
+      small[(int64_t)a.D * (a.S + 1) + blk.c0 + c] = y;
     }
     return;
   }
 
   constexpr int CW = 32 / L;  // channels a warp, in the low lane bits
-  constexpr bool TENSOR = L == 4 && sizeof(IO) == 2;
   const int warp = tid / 32, lane = tid % 32, l = lane / CW, ch = warp * CW + lane % CW;
   const bool on = ch < blk.n;
   const int d = blk.c0 + (on ? ch : 0), n0 = l * kSsmStates;
@@ -332,19 +338,32 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   for (int i = 0; i < kSsmStates; ++i) {
     const bool real = on && n0 + i < a.S;
     A2[i] = real ? a.A[(int64_t)d * a.S + n0 + i] * kLog2e : 0.f;
-    g0[i] = real && b.d_final ? b.d_final[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
+    g0[i] = real && b.d_final && !ENDS ? b.d_final[((int64_t)seq * a.D + d) * a.S + n0 + i] : 0.f;
+  }
+  if (cut && !ENDS) {  // through the segments behind this one
+    const int n = (int)(((int64_t)seq_end - seq_start + split.seg - 1) / split.seg);
+    for (int k = n - 1; k > piece; --k) {
+      const int64_t row = (id - piece + k) * a.D + d;
+      const float sum = split.steps[row];
+#pragma unroll
+      for (int i = 0; i < kSsmStates; ++i)
+        if (on && n0 + i < a.S)
+          g0[i] = fmaf(ex2_f(sum * A2[i]), g0[i], split.ends[row * a.S + n0 + i]);
+    }
   }
   const f32x2 A01 = pack2(A2[0], A2[1]), A23 = pack2(A2[2], A2[3]);
   f32x2 dh01 = pack2(g0[0], g0[1]), dh23 = pack2(g0[2], g0[3]);
   f32x2 dA01 = both(0.f), dA23 = both(0.f);
+  float steps = 0.f;
   auto fetch = [&](int i, int w) {  // the start states of tile i's chunks
-    if (!st_vec || !on || n0 >= a.S) return;
+    if (ENDS || !st_vec || !on || n0 >= a.S) return;
     const int t0 = i * kTile, m = min(kTile, end - start - t0);
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
       if (c * K < m) {
         const float* p = part.states +
-                         (ssm_piece_id(seq, start, K, t0 / K + c) * a.D + d) * a.S + n0;
+                         (ssm_piece_id(seq, seq_start, K, (start - seq_start + t0) / K + c) * a.D + d) *
+                             a.S + n0;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::
                      "r"((unsigned)__cvta_generic_to_shared(&sh.state[w][c][tid])), "l"(p));
       }
@@ -360,6 +379,21 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     if (PARTS == 1) __syncthreads();
     for (int c = (m - 1) / K; c >= 0; --c) {
       const int tc = c * K;
+      if constexpr (ENDS) {
+#pragma unroll
+        for (int t = K - 1; t >= 0; --t) {
+          const float dt = sh.dt[w][tc + t][t & 1 ? slot1 : slot0].x;
+          const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sh.c[w][tc + t][n0]);
+          const f32x2 dy = both(sh.dy[w][tc + t][ch]);
+          float p[4];
+          unpack2(mul2(both(dt), A01), p[0], p[1]);
+          unpack2(mul2(both(dt), A23), p[2], p[3]);
+          dh01 = mul2(fma2(dy, cv.x, dh01), pack2(ex2_f(p[0]), ex2_f(p[1])));
+          dh23 = mul2(fma2(dy, cv.y, dh23), pack2(ex2_f(p[2]), ex2_f(p[3])));
+          steps += dt;
+        }
+        continue;
+      }
       f32x2 h01[K + 1], h23[K + 1], e01[K], e23[K];
       if (st_vec) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -368,7 +402,9 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         h23[0] = pack2(v.z, v.w);
       } else {
         const float* p =
-            part.states + (ssm_piece_id(seq, start, K, i * CHUNKS + c) * a.D + d) * a.S + n0;
+            part.states +
+            (ssm_piece_id(seq, seq_start, K, (start - seq_start) / K + i * CHUNKS + c) * a.D + d) *
+                a.S + n0;
         float v[kSsmStates];
 #pragma unroll
         for (int k = 0; k < kSsmStates; ++k) v[k] = on && n0 + k < a.S ? p[k] : 0.f;
@@ -389,7 +425,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         h23[t + 1] = fma2(e23[t], h23[t], mul2(dtu, bv.y));
       }
       f32x2 s01 = both(0.f), s23 = both(0.f);  // dA of the chunk
-      float fed[4], qa[4], sums[4];
+      float fed[4], qa[4];
 #pragma unroll
       for (int t = K - 1; t >= 0; --t) {
         const float2 v = sh.dt[w][tc + t][t & 1 ? slot1 : slot0];
@@ -410,22 +446,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         qa[t & 3] = sum2(fma2(q01, A01, mul2(q23, A23)));
         s01 = fma2(q01, dt, s01);
         s23 = fma2(q23, dt, s23);
-        if constexpr (TENSOR) {
-          // tokens t (odd) and t - 1: product 4 (t & 1) + j adds dB_j into row
-          // 4 (t & 1) + j and dC_j into the row 8 below, for the state groups
-          // and the channels' two halves as columns
-          if (t & 1) sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t one = lane / 4 == (t & 1) * 4 + j ? 0x3f800000u : 0u;
-            mma_tf32(sums, one, 0u, 0u, one, bc[j], bc[4 + j]);
-          }
-          if (!(t & 1)) {
-            const int q = lane / 4, at = lane % 4 * 4 + (q & 3);
-            sh.part[w % PARTS][warp][tc + t + q / 4][0][at] = sums[0] + sums[1];
-            sh.part[w % PARTS][warp][tc + t + q / 4][1][at] = sums[2] + sums[3];
-          }
-        } else {
+        {
           int f = 0;
           SpreadSum<8, 1, CW>::run(bc, lane, f);
           constexpr int LEFT = 8 / CW > 1 ? 8 / CW : 1;
@@ -459,10 +480,14 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
 #pragma unroll
   for (int k = 0; k < kSsmStates; ++k) {
     if (!on || n0 + k >= a.S) continue;
-    const int64_t at = ((int64_t)seq * a.D + d) * a.S + n0 + k;
-    part.dA[at] = dA[k];
-    if (b.dh0) b.dh0[at] = dh[k];
+    if (ENDS) {
+      split.ends[(id * a.D + d) * a.S + n0 + k] = dh[k];
+      continue;
+    }
+    small[(int64_t)d * a.S + n0 + k] = dA[k];
+    if (b.dh0 && piece == 0) b.dh0[((int64_t)seq * a.D + d) * a.S + n0 + k] = dh[k];
   }
+  if (ENDS && on && l == 0) split.steps[id * a.D + d] = steps;
 }
 
 // dB and dC of a token's group: the channel blocks' parts.
@@ -485,33 +510,53 @@ __global__ void ssm_bc_sum_kernel(SsmBwdArgs b, const float* __restrict__ bc, in
   out[(tok * a.G + g) * a.S + e % a.S] = from_f32<IO>(s);
 }
 
-// out[i] = sum over sequences of part[seq][i]
-__global__ void ssm_seq_sum_kernel(const float* __restrict__ part, int n_seqs, int64_t n,
-                                   float* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (int k = 0; k < n_seqs; ++k) s += part[k * n + i];
-  out[i] = s;
+// dA, dskip and dbias: the segments' parts, 8 rows of threads and then their
+// sums in order.
+__global__ void ssm_small_sum_kernel(const float* __restrict__ part, int64_t ids, int D, int S,
+                                     float* __restrict__ dA, float* __restrict__ dskip,
+                                     float* __restrict__ dbias) {
+  __shared__ float s[8][32];
+  const int64_t n = (int64_t)D * (S + 2), i = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (i < n)
+    for (int64_t k = threadIdx.y; k < ids; k += 8) v += part[k * n + i];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y || i >= n) return;
+  for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+  const int64_t m = (int64_t)D * S;
+  if (i < m)
+    dA[i] = v;
+  else if (i < m + D) {
+    if (dskip) dskip[i - m] = v;
+  } else if (dbias) {
+    dbias[i - m - D] = v;
+  }
 }
 
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// A backward's segments: its passes over the recurrence cost about three times
+// a split's, so two segments a sequence are worth it.
+int bwd_segment(const SsmBwdArgs& b, int sms) { return ssm_segment(b.f, sms, 2.0); }
+int64_t bwd_ids(const SsmArgs& a, int seg) {
+  return seg == INT32_MAX ? a.n_seqs : ssm_segments(a, seg);
+}
+
 struct Layout {
-  size_t states, bc, dA, dskip, dbias, total;
+  size_t states, bc, small, fwd_ends, bwd_ends, total;
 };
-Layout layout(const SsmBwdArgs& b) {
+Layout layout(const SsmBwdArgs& b, int seg) {
   const SsmArgs& a = b.f;
-  const size_t ids = (size_t)a.tokens / kSsmChunk + a.n_seqs + 1;
-  // dense sequences count their chunks by the same ids
+  const size_t chunks = (size_t)a.tokens / kSsmChunk + a.n_seqs + 1;
   const size_t blocks = ssm_blocks(a, kSsmThreads / ssm_lanes(a.S));
   Layout o;
   o.states = 0;
-  o.bc = o.states + up(ids * a.D * a.S * 4);
-  o.dA = o.bc + up(blocks * a.tokens * 2 * a.S * 4);
-  o.dskip = o.dA + up((size_t)a.n_seqs * a.D * a.S * 4);
-  o.dbias = o.dskip + up((size_t)a.n_seqs * a.D * 4);
-  o.total = o.dbias + up((size_t)a.n_seqs * a.D * 4);
+  o.bc = o.states + up(chunks * a.D * a.S * 4);
+  o.small = o.bc + up(blocks * a.tokens * 2 * a.S * 4);
+  o.fwd_ends = o.small + up((size_t)bwd_ids(a, seg) * a.D * (a.S + 2) * 4);
+  o.bwd_ends = o.fwd_ends + up(ssm_split_bytes(a, seg));
+  o.total = o.bwd_ends + up(ssm_split_bytes(a, seg));
   return o;
 }
 
@@ -525,18 +570,28 @@ bool vec_ok(const SsmBwdArgs& b) {
          a.z_stride % E == 0;
 }
 
-template <typename IO, int L>
-cudaError_t bwd_launch(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st) {
-  const unsigned grid = (unsigned)ssm_blocks(b.f, kSsmThreads / L) * (unsigned)b.f.n_seqs;
-  if (!grid) return cudaSuccess;
+template <typename IO, int L, bool ENDS>
+cudaError_t pass_launch(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st) {
+  const unsigned grid =
+      (unsigned)(bwd_ids(b.f, part.split.seg) * ssm_blocks(b.f, kSsmThreads / L));
   constexpr int E = tile_of(L) * (kSsmThreads / L) / kHelpers;
-  auto* k = vec_ok<IO, E>(b) ? ssm_bwd_kernel<IO, L, true> : ssm_bwd_kernel<IO, L, false>;
+  auto* k = vec_ok<IO, E>(b) ? ssm_bwd_kernel<IO, L, true, ENDS>
+                             : ssm_bwd_kernel<IO, L, false, ENDS>;
   constexpr int bytes = sizeof(BwdShared<L>);
   static_assert(bytes <= 227 * 1024, "shared memory of an SM");
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   k<<<grid, kSsmThreads + kHelpers, bytes, st>>>(b, part);
   return cudaGetLastError();
+}
+template <typename IO, int L>
+cudaError_t bwd_launch(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st) {
+  if (b.f.n_seqs == 0) return cudaSuccess;
+  if (part.split.seg != INT32_MAX) {
+    const cudaError_t e = pass_launch<IO, L, true>(b, part, st);
+    if (e != cudaSuccess) return e;
+  }
+  return pass_launch<IO, L, false>(b, part, st);
 }
 
 template <typename IO>
@@ -556,35 +611,33 @@ cudaError_t bwd_pick(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st)
   return cudaGetLastError();
 }
 
-cudaError_t seq_sum(const float* part, const SsmArgs& a, int64_t n, float* out, cudaStream_t st) {
-  if (!out) return cudaSuccess;
-  ssm_seq_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, a.n_seqs, n, out);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
-size_t ssm_bwd_workspace_bytes(const SsmBwdArgs& b) { return layout(b).total; }
-
-int ssm_bwd_kernel_count(const SsmBwdArgs& b) {
-  return (b.f.n_seqs ? 2 : 0) + (b.f.tokens ? 1 : 0) + 1 + (b.dskip ? 1 : 0) + (b.dbias ? 1 : 0);
+size_t ssm_bwd_workspace_bytes(const SsmBwdArgs& b, int sms) {
+  return layout(b, bwd_segment(b, sms)).total;
 }
 
-cudaError_t launch_ssm_bwd(const SsmBwdArgs& b, void* ws, cudaStream_t st) {
-  const Layout o = layout(b);
+int ssm_bwd_kernel_count(const SsmBwdArgs& b, int sms) {
+  const bool cut = bwd_segment(b, sms) != INT32_MAX;
+  return (b.f.n_seqs ? cut ? 4 : 2 : 0) + (b.f.tokens ? 1 : 0) + 1;
+}
+
+cudaError_t launch_ssm_bwd(const SsmBwdArgs& b, void* ws, int sms, cudaStream_t st) {
+  const int seg = bwd_segment(b, sms);
+  const Layout o = layout(b, seg);
   char* w = static_cast<char*>(ws);
-  BwdParts part{reinterpret_cast<float*>(w + o.states), reinterpret_cast<float*>(w + o.bc),
-                reinterpret_cast<float*>(w + o.dA), reinterpret_cast<float*>(w + o.dskip),
-                reinterpret_cast<float*>(w + o.dbias)};
-  SsmSave save{part.states, b.d_out, b.f.z ? b.dz : nullptr};
-  const SsmSplit whole{INT32_MAX, nullptr, nullptr};
-  cudaError_t e = launch_ssm_save(b.f, save, whole, st);
+  const BwdParts part{reinterpret_cast<float*>(w + o.states), reinterpret_cast<float*>(w + o.bc),
+                      reinterpret_cast<float*>(w + o.small),
+                      ssm_split_at(b.f, seg, w + o.bwd_ends)};
+  const SsmSave save{part.states, b.d_out, b.f.z ? b.dz : nullptr};
+  cudaError_t e = launch_ssm_save(b.f, save, ssm_split_at(b.f, seg, w + o.fwd_ends), st);
   if (e == cudaSuccess)
     e = b.f.bf16 ? bwd_pick<__nv_bfloat16>(b, part, st) : bwd_pick<float>(b, part, st);
-  if (e == cudaSuccess) e = seq_sum(part.dA, b.f, (int64_t)b.f.D * b.f.S, b.dA, st);
-  if (e == cudaSuccess) e = seq_sum(part.dskip, b.f, b.f.D, b.dskip, st);
-  if (e == cudaSuccess) e = seq_sum(part.dbias, b.f, b.f.D, b.dbias, st);
-  return e;
+  if (e != cudaSuccess) return e;
+  const int64_t n = (int64_t)b.f.D * (b.f.S + 2);
+  ssm_small_sum_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 8), 0, st>>>(
+      part.small, bwd_ids(b.f, seg), b.f.D, b.f.S, b.dA, b.dskip, b.dbias);
+  return cudaGetLastError();
 }
 
 }  // namespace kda

@@ -165,7 +165,8 @@ KDA_API kda_status kda_ssm_scan_bwd(
     cudaStream_t stream);
 
 /* Kernels a kda_ssm_scan_bwd call of this shape launches and the workspace
- * it allocates; no device work.  `packed` selects the cu_seqlens layout. */
+ * it allocates on the current device (148 SMs where there is none); no device
+ * work.  `packed` selects the cu_seqlens layout. */
 KDA_API kda_status kda_ssm_scan_bwd_plan(const kda_ssm_shape* shape,
                                          int packed, int* kernels,
                                          size_t* workspace_bytes);

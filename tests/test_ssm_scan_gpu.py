@@ -373,3 +373,32 @@ def test_split_in_place_and_repeated():
         st = d["past"].clone()
         out2, _ = K.ssm_scan_fwd(*args, initial_state=st, final_state=st)
         assert torch.equal(out, out2) and torch.equal(fin, st)
+
+
+def test_split_backward_repeats_and_matches_one_segment():
+    # a sequence in segments, and the same sequence in a batch wide enough
+    # not to be split (its copies): other roundings at the joins only
+    T, D, S = 1500, 64, 16
+    d = make((1, T), D, S, 1, "f32", 33, past=1)
+    kw = dict(D=d["D"], z=d["z"], delta_bias=d["delta_bias"],
+              initial_state=d["past"], d_out=d["d_out"],
+              d_final_state=d["d_final"])
+    args = (d["u"], d["delta"], d["A"], d["Bm"], d["Cm"])
+    a = K.ssm_scan_bwd(*args, **kw)
+    for _ in range(2):
+        b = K.ssm_scan_bwd(*args, **kw)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    n = 200
+
+    def many(t):
+        return t.expand(n, *t.shape[1:]).contiguous()
+    kw.update(z=many(d["z"]), initial_state=many(d["past"]),
+              d_out=many(d["d_out"]), d_final_state=many(d["d_final"]))
+    c = K.ssm_scan_bwd(many(d["u"]), many(d["delta"]), d["A"], many(d["Bm"]),
+                       many(d["Cm"]), **kw)
+    for name, x, y in zip(NAMES, a, c):
+        if name in ("A", "D", "delta_bias"):
+            y = y / n  # a sum of n equal terms, rounded n times at most
+            R.check("d " + name, x, y.cpu().double(), 4 * tol(T) + n * 2.0 ** -24)
+        else:
+            R.check("d " + name, x, y[:1].cpu().double(), 4 * tol(T))
