@@ -8,6 +8,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -43,14 +45,26 @@ def nvcc():
 
 
 def build(force=False, verbose=False, extra=()):
+    """Compiles the sources side by side (nvcc takes one core a source) and
+    links them."""
     if not force and not _stale():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-shared", "-I",
-           os.path.join(ROOT, "include"), "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.check_call(cmd)
+
+    with tempfile.TemporaryDirectory() as objs:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            run([nvcc(), *NVCC_FLAGS, *extra, "-I",
+                 os.path.join(ROOT, "include"), "-c", "-o", obj, src])
+            return obj
+        with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+            done = list(pool.map(compile_one, sources()))
+        run([nvcc(), *NVCC_FLAGS[:2], "-shared", "-o", tmp, *done])
     os.replace(tmp, LIB)
     return LIB
 

@@ -83,48 +83,11 @@ struct RowSum {
   }
 };
 
-// Element offsets of a thread's vectors and the rows of its block.
-template <int VEC, int ITER>
-struct Place {
-  int rows_per_block, sub, col0, stride, width;
-  __device__ __forceinline__ Place(int tpr, int width_) {
-    sub = threadIdx.x / tpr;
-    rows_per_block = blockDim.x / tpr;
-    col0 = threadIdx.x % tpr * VEC;
-    stride = tpr * VEC;
-    width = width_;
-  }
-  __device__ __forceinline__ int col(int i) const { return col0 + i * stride; }
-  __device__ __forceinline__ bool on(int i) const { return col(i) < width; }
-};
-
-// A weight's values at a thread's columns, or 1 without the weight.  The
-// pointers may be 4-byte aligned only (then not `vec`).
-template <int VEC>
-__device__ __forceinline__ void weight_at(const float* w, bool vec, int col,
-                                          f32x2 (&v)[kPairs<VEC>]) {
-  if (!w) {
-#pragma unroll
-    for (int i = 0; i < kPairs<VEC>; ++i) v[i] = both(1.f);
-  } else if (VEC >= 4 && vec) {
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(w + col) + i);
-      v[2 * i % kPairs<VEC>] = pack2(t.x, t.y);
-      v[(2 * i + 1) % kPairs<VEC>] = pack2(t.z, t.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPairs<VEC>; ++i)
-      v[i] = pack2(__ldg(w + col + 2 * i), VEC > 1 ? __ldg(w + col + 2 * i + 1) : 0.f);
-  }
-}
-
 // A row's elements pass once: they do not stay in L1.
-template <typename T, int VEC>
-__device__ __forceinline__ Raw<T, VEC> load_once(const T* p) {
-  constexpr int BYTES = VEC * (int)sizeof(T);
-  Raw<T, VEC> r;
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> load_once(const T* p) {
+  constexpr int BYTES = N * (int)sizeof(T);
+  Raw<T, N> r;
   if constexpr (BYTES % 16 == 0) {
     uint4* q = reinterpret_cast<uint4*>(&r);
 #pragma unroll
@@ -133,21 +96,131 @@ __device__ __forceinline__ Raw<T, VEC> load_once(const T* p) {
                    : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
                    : "l"(reinterpret_cast<const uint4*>(p) + i));
   } else {
-    r = load_raw<T, VEC>(p);
+    r = load_raw<T, N>(p);
   }
   return r;
 }
 
-// `row`: the row's first element, or null.
-template <typename T, int VEC, int ITER>
-__device__ __forceinline__ void load_row(const T* row, const Place<VEC, ITER>& p,
-                                         Raw<T, VEC> (&v)[ITER]) {
-#pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    v[i] = Raw<T, VEC>{};
-    if (row && p.on(i)) v[i] = load_once<T, VEC>(row + p.col(i));
+// What a thread holds of its row: ITER vectors of VEC elements, each in
+// accesses of UNIT neighbouring elements (VEC where rows are aligned, 2 where
+// only the width is even, else 1); access k of vector i starts at column
+// (lane + (i VEC / UNIT + k) TPR) UNIT, so that a warp's accesses are next to
+// each other.  Elements behind the row's end load as 0 and are not stored.
+template <int VEC, int ITER, int UNIT>
+struct Place {
+  static constexpr int P = VEC / 2, N = VEC / UNIT;
+  int rows_per_block, sub, col0, stride, width;
+  __device__ __forceinline__ Place(int tpr, int width_) {
+    sub = threadIdx.x / tpr;
+    rows_per_block = blockDim.x / tpr;
+    col0 = threadIdx.x % tpr * UNIT;
+    stride = tpr * UNIT;
+    width = width_;
   }
-}
+  __device__ __forceinline__ int col(int i, int k) const { return col0 + (i * N + k) * stride; }
+  __device__ __forceinline__ bool on(int i, int k) const { return col(i, k) < width; }
+
+  template <typename T>
+  struct Row {  // as loaded
+    Raw<T, UNIT> v[ITER][N];
+  };
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, Row<T>& r) const {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        r.v[i][k] = Raw<T, UNIT>{};
+        if (row && on(i, k)) r.v[i][k] = load_once<T, UNIT>(row + col(i, k));
+      }
+  }
+  template <typename T>
+  __device__ __forceinline__ static void unpack_row(const Row<T>& r, int i, f32x2 (&v)[P]) {
+    float f[VEC];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float u[UNIT];
+      unpack(r.v[i][k], u);
+#pragma unroll
+      for (int j = 0; j < UNIT; ++j) f[k * UNIT + j] = u[j];
+    }
+#pragma unroll
+    for (int c = 0; c < P; ++c) v[c] = pack2(f[2 * c], f[2 * c + 1]);
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int i, const f32x2 (&v)[P]) const {
+    float f[VEC];
+#pragma unroll
+    for (int c = 0; c < P; ++c) unpack2(v[c], f[2 * c], f[2 * c + 1]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float u[UNIT];
+#pragma unroll
+      for (int j = 0; j < UNIT; ++j) u[j] = f[k * UNIT + j];
+      if (on(i, k)) store_vec<T, UNIT>(row + col(i, k), u);
+    }
+  }
+  // a weight's values, or 1 without it; `vec`: 16-byte aligned
+  __device__ __forceinline__ void weight(const float* w, bool vec, int i, f32x2 (&v)[P]) const {
+    if (!w) {
+#pragma unroll
+      for (int c = 0; c < P; ++c) v[c] = both(1.f);
+      return;
+    }
+    float f[VEC];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float* q = w + col(i, k);
+      const bool real = on(i, k);
+      if (UNIT >= 4 && vec) {
+#pragma unroll
+        for (int j = 0; j < UNIT; j += 4) {
+          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (real) t = __ldg(reinterpret_cast<const float4*>(q + j));
+          f[k * UNIT + j] = t.x;
+          f[(k * UNIT + j + 1) % VEC] = t.y;
+          f[(k * UNIT + j + 2) % VEC] = t.z;
+          f[(k * UNIT + j + 3) % VEC] = t.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) f[k * UNIT + j] = real ? __ldg(q + j) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < P; ++c) v[c] = pack2(f[2 * c], f[2 * c + 1]);
+  }
+  // s[columns] += t u, in shared memory that no other thread touches
+  __device__ __forceinline__ void add(float* s, int i, const f32x2 (&t)[P],
+                                      const f32x2 (&u)[P]) const {
+    if constexpr (UNIT >= 4) {
+#pragma unroll
+      for (int j = 0; j < VEC / 4; ++j) {
+        if (!on(i, 0)) break;
+        ulonglong2* q = reinterpret_cast<ulonglong2*>(s + col(i, 0)) + j;
+        ulonglong2 v = *q;
+        v.x = fma2(t[2 * j], u[2 * j], v.x);
+        v.y = fma2(t[2 * j + 1], u[2 * j + 1], v.y);
+        *q = v;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        float lo, hi;
+        unpack2(mul2(t[c], u[c]), lo, hi);
+        if (UNIT == 2) {
+          if (!on(i, c)) break;
+          float2* q = reinterpret_cast<float2*>(s + col(i, c));
+          const float2 v = *q;
+          *q = make_float2(v.x + lo, v.y + hi);
+        } else {
+          if (on(i, 2 * c)) s[col(i, 2 * c)] += lo;
+          if (on(i, 2 * c + 1)) s[col(i, 2 * c + 1)] += hi;
+        }
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ int64_t strided(const NormArgs& a, int64_t row, int64_t stride) {
   if (a.heads == 1) return row * stride;
@@ -161,11 +234,12 @@ __device__ __forceinline__ bool aligned16(const void* a, const void* b, const vo
 }
 
 // GATE: 0 none, 1 behind the norm, 2 before it.
-template <typename IO, typename RT, int VEC, int ITER, int GATE>
+template <typename IO, typename RT, int VEC, int ITER, int UNIT, int GATE>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
-  constexpr int P = kPairs<VEC>;
+  using At = Place<VEC, ITER, UNIT>;
+  constexpr int P = At::P;
   __shared__ float4 s_sum[32];
-  const Place<VEC, ITER> p(tpr, a.width);
+  const At p(tpr, a.width);
   RowSum sum{tpr, 0, s_sum};
   const Gate act{a.act == kActNone, a.act == kActSilu};
   const int64_t rows = a.tokens * a.heads;
@@ -178,21 +252,21 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
        base += (int64_t)gridDim.x * p.rows_per_block) {
     const int64_t row = base + p.sub, at = row * a.width;
     const bool row_on = row < rows;
-    Raw<IO, VEC> rx[ITER], rg[GATE ? ITER : 1];
-    Raw<RT, VEC> rr[ITER];
-    load_row<IO>(row_on ? x + strided(a, row, a.x_stride) : nullptr, p, rx);
+    typename At::template Row<IO> rx, rg;
+    typename At::template Row<RT> rr;
+    p.load(row_on ? x + strided(a, row, a.x_stride) : nullptr, rx);
     if constexpr (GATE != 0)
-      load_row<IO>(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, p, rg);
-    load_row<RT>(row_on && res ? res + at : nullptr, p, rr);
+      p.load(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, rg);
+    p.load(row_on && res ? res + at : nullptr, rr);
     f32x2 h[ITER][P];
     float s[1];
     f32x2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      unpack_pairs<IO, VEC>(rx[i], h[i]);
+      p.unpack_row(rx, i, h[i]);
       if constexpr (GATE == 2) {
         f32x2 g[P];
-        unpack_pairs<IO, VEC>(rg[i], g);
+        p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) h[i][c] = mul2(h[i][c], act.f(g[c]));
       }
@@ -208,16 +282,15 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
     acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      if (!p.on(i)) continue;
       f32x2 w[P], sc[P], r[P];
-      weight_at<VEC>(a.post_weight, wvec, p.col(i), w);
-      weight_at<VEC>(a.scale, wvec, p.col(i), sc);
-      unpack_pairs<RT, VEC>(rr[i], r);
+      p.weight(a.post_weight, wvec, i, w);
+      p.weight(a.scale, wvec, i, sc);
+      p.unpack_row(rr, i, r);
 #pragma unroll
       for (int c = 0; c < P; ++c) h[i][c] = mul2(mul2(h[i][c], both(r1)), w[c]);
       if constexpr (GATE == 1) {
         f32x2 g[P];
-        unpack_pairs<IO, VEC>(rg[i], g);
+        p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) h[i][c] = mul2(h[i][c], act.f(g[c]));
       }
@@ -226,7 +299,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
         h[i][c] = fma2(sc[c], h[i][c], r[c]);
         acc = fma2(h[i][c], h[i][c], acc);
       }
-      if (row_on) store_pairs<RT, VEC>(static_cast<RT*>(a.out) + at + p.col(i), h[i]);
+      if (row_on) p.store(static_cast<RT*>(a.out) + at, i, h[i]);
     }
     if (a.pre_weight) {
       s[0] = sum2(acc);
@@ -234,44 +307,26 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormArgs a, int tpr) {
       const float r2 = rsqrtf(s[0] * inv_w + a.eps);
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        if (!p.on(i)) continue;
-        f32x2 w[P];
-        weight_at<VEC>(a.pre_weight, wvec, p.col(i), w);
+          f32x2 w[P];
+        p.weight(a.pre_weight, wvec, i, w);
 #pragma unroll
         for (int c = 0; c < P; ++c) h[i][c] = mul2(mul2(h[i][c], both(r2)), w[c]);
-        if (row_on) store_pairs<IO, VEC>(static_cast<IO*>(a.normed) + at + p.col(i), h[i]);
+        if (row_on) p.store(static_cast<IO*>(a.normed) + at, i, h[i]);
       }
     }
   }
 }
 
-// s[0 .. VEC) += t u, a thread's own columns in shared memory
-template <int VEC>
-__device__ __forceinline__ void add_columns(float* s, const f32x2 (&t)[kPairs<VEC>],
-                                            const f32x2 (&u)[kPairs<VEC>]) {
-  if constexpr (VEC >= 4) {
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      ulonglong2* q = reinterpret_cast<ulonglong2*>(s) + i;
-      ulonglong2 v = *q;
-      v.x = fma2(t[2 * i], u[2 * i], v.x);
-      v.y = fma2(t[2 * i + 1], u[2 * i + 1], v.y);
-      *q = v;
-    }
-  } else {
-    s[0] += sum2(mul2(t[0], u[0]));  // the pair's other half is 0
-  }
-}
-
 // part[block * rows_per_block + sub][3][width]: the weights' gradients of one
 // row place's rows; norm_weight_sum_kernel sums them in a fixed order.
-template <typename IO, typename RT, int VEC, int ITER, int GATE>
+template <typename IO, typename RT, int VEC, int ITER, int UNIT, int GATE>
 __global__ void __launch_bounds__(512)
     norm_bwd_kernel(NormArgs a, int tpr, float* __restrict__ part) {
-  constexpr int P = kPairs<VEC>;
+  using At = Place<VEC, ITER, UNIT>;
+  constexpr int P = At::P;
   __shared__ float4 s_sum[32];
   extern __shared__ __align__(16) float s_cols[];  // [rows of the block][3][padded width]
-  const Place<VEC, ITER> p(tpr, a.width);
+  const At p(tpr, a.width);
   RowSum sum{tpr, 0, s_sum};
   const Gate act{a.act == kActNone, a.act == kActSilu};
   const int64_t rows = a.tokens * a.heads;
@@ -283,9 +338,14 @@ __global__ void __launch_bounds__(512)
   float* c_pre = c_scale + pitch;
 #pragma unroll
   for (int i = 0; i < ITER; ++i)
-    if (p.on(i))
-      for (int c = 0; c < VEC; ++c)
-        c_post[p.col(i) + c] = c_scale[p.col(i) + c] = c_pre[p.col(i) + c] = 0.f;
+#pragma unroll
+    for (int e = 0; e < At::N; ++e)
+      if (p.on(i, e))
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) {
+          const int c = p.col(i, e) + j;
+          c_post[c] = c_scale[c] = c_pre[c] = 0.f;
+        }
   const IO* x = static_cast<const IO*>(a.x);
   const IO* gate = static_cast<const IO*>(a.gate);
   const RT* res = static_cast<const RT*>(a.residual);
@@ -296,22 +356,22 @@ __global__ void __launch_bounds__(512)
        base += (int64_t)gridDim.x * p.rows_per_block) {
     const int64_t row = base + p.sub, at = row * a.width;
     const bool row_on = row < rows;
-    Raw<IO, VEC> rx[ITER], rg[GATE ? ITER : 1], rn[ITER];
-    Raw<RT, VEC> rr[ITER], ro[ITER];
-    load_row<IO>(row_on ? x + strided(a, row, a.x_stride) : nullptr, p, rx);
+    typename At::template Row<IO> rx, rg, rn;
+    typename At::template Row<RT> rr, ro;
+    p.load(row_on ? x + strided(a, row, a.x_stride) : nullptr, rx);
     if constexpr (GATE != 0)
-      load_row<IO>(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, p, rg);
-    load_row<IO>(row_on && pre ? dnorm + at : nullptr, p, rn);
-    load_row<RT>(row_on && pre && res ? res + at : nullptr, p, rr);
-    load_row<RT>(row_on && dout ? dout + at : nullptr, p, ro);
+      p.load(row_on ? gate + strided(a, row, a.gate_stride) : nullptr, rg);
+    p.load(row_on && pre ? dnorm + at : nullptr, rn);
+    p.load(row_on && pre && res ? res + at : nullptr, rr);
+    p.load(row_on && dout ? dout + at : nullptr, ro);
     // sg: sigmoid(gate); hat: x [act(gate)] r1; d: the gradient from out to x
     f32x2 sg[GATE ? ITER : 1][P], out[ITER][P], d[ITER][P];
     float r1 = 1.f;
     auto h_of = [&](int i, f32x2(&h)[P]) {
-      unpack_pairs<IO, VEC>(rx[i], h);
+      p.unpack_row(rx, i, h);
       if constexpr (GATE == 2) {
         f32x2 g[P], f, fd;
-        unpack_pairs<IO, VEC>(rg[i], g);
+        p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) {
           act.fd(g[c], sg[i][c], f, fd);
@@ -323,7 +383,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         f32x2 g[P];
-        unpack_pairs<IO, VEC>(rg[i], g);
+        p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) sg[i][c] = act.none ? both(0.f) : sigmoid2(g[c]);
       }
@@ -346,16 +406,15 @@ __global__ void __launch_bounds__(512)
       f32x2 acc1 = both(0.f), acc2 = both(0.f);
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        if (!p.on(i)) continue;
         f32x2 w[P], sc[P], wn[P], h[P], n[P], r[P];
-        weight_at<VEC>(a.post_weight, wvec, p.col(i), w);
-        weight_at<VEC>(a.scale, wvec, p.col(i), sc);
-        weight_at<VEC>(a.pre_weight, wvec, p.col(i), wn);
+        p.weight(a.post_weight, wvec, i, w);
+        p.weight(a.scale, wvec, i, sc);
+        p.weight(a.pre_weight, wvec, i, wn);
         h_of(i, h);
-        unpack_pairs<IO, VEC>(rn[i], n);
-        unpack_pairs<RT, VEC>(rr[i], r);
+        p.unpack_row(rn, i, n);
+        p.unpack_row(rr, i, r);
         f32x2 g[P];
-        if constexpr (GATE == 1) unpack_pairs<IO, VEC>(rg[i], g);
+        if constexpr (GATE == 1) p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) {
           f32x2 q = mul2(mul2(h[c], both(r1)), w[c]);
@@ -378,28 +437,26 @@ __global__ void __launch_bounds__(512)
     f32x2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      if (!p.on(i)) continue;
-      const int col = p.col(i);
-      unpack_pairs<RT, VEC>(ro[i], d[i]);
+      p.unpack_row(ro, i, d[i]);
       if (pre) {
         f32x2 wn[P], n[P], o2[P];
-        weight_at<VEC>(a.pre_weight, wvec, col, wn);
-        unpack_pairs<IO, VEC>(rn[i], n);
+        p.weight(a.pre_weight, wvec, i, wn);
+        p.unpack_row(rn, i, n);
 #pragma unroll
         for (int c = 0; c < P; ++c) {
           d[i][c] = fma2(both(r2), fma2(out[i][c], both(m2), mul2(n[c], wn[c])), d[i][c]);
           o2[c] = mul2(out[i][c], both(r2));
         }
-        add_columns<VEC>(c_pre + col, n, o2);
+        p.add(c_pre, i, n, o2);
       }
-      if (a.dres && row_on) store_pairs<RT, VEC>(static_cast<RT*>(a.dres) + at + col, d[i]);
+      if (a.dres && row_on) p.store(static_cast<RT*>(a.dres) + at, i, d[i]);
       f32x2 w[P], sc[P], h[P], q[P], f[P], fd[P];
-      weight_at<VEC>(a.post_weight, wvec, col, w);
-      weight_at<VEC>(a.scale, wvec, col, sc);
+      p.weight(a.post_weight, wvec, i, w);
+      p.weight(a.scale, wvec, i, sc);
       h_of(i, h);
       if constexpr (GATE == 1) {
         f32x2 g[P];
-        unpack_pairs<IO, VEC>(rg[i], g);
+        p.unpack_row(rg, i, g);
 #pragma unroll
         for (int c = 0; c < P; ++c) act.fd(g[c], sg[i][c], f[c], fd[c]);
       }
@@ -412,7 +469,7 @@ __global__ void __launch_bounds__(512)
           q[c] = mul2(q[c], f[c]);
         }
       }
-      if (a.dscale) add_columns<VEC>(c_scale + col, d[i], q);
+      if (a.dscale) p.add(c_scale, i, d[i], q);
 #pragma unroll
       for (int c = 0; c < P; ++c) {
         d[i][c] = mul2(d[i][c], sc[c]);
@@ -422,8 +479,8 @@ __global__ void __launch_bounds__(512)
         }
       }
       if constexpr (GATE == 1)
-        if (row_on) store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + col, fd);
-      if (a.dpost) add_columns<VEC>(c_post + col, d[i], h);
+        if (row_on) p.store(static_cast<IO*>(a.dgate) + at, i, fd);
+      if (a.dpost) p.add(c_post, i, d[i], h);
 #pragma unroll
       for (int c = 0; c < P; ++c) {
         d[i][c] = mul2(d[i][c], w[c]);
@@ -438,8 +495,7 @@ __global__ void __launch_bounds__(512)
     }
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      if (!p.on(i) || !row_on) continue;
-      const int col = p.col(i);
+      if (!row_on) continue;
       if (a.post_weight) {
         f32x2 h[P];
         h_of(i, h);
@@ -449,8 +505,8 @@ __global__ void __launch_bounds__(512)
       }
       if constexpr (GATE == 2) {  // d is the gradient of h = x act(g)
         f32x2 g[P], xv[P], dg[P];
-        unpack_pairs<IO, VEC>(rg[i], g);
-        unpack_pairs<IO, VEC>(rx[i], xv);
+        p.unpack_row(rg, i, g);
+        p.unpack_row(rx, i, xv);
 #pragma unroll
         for (int c = 0; c < P; ++c) {
           f32x2 f, fd;
@@ -458,21 +514,24 @@ __global__ void __launch_bounds__(512)
           dg[c] = mul2(mul2(fd, xv[c]), d[i][c]);
           d[i][c] = mul2(d[i][c], f);
         }
-        store_pairs<IO, VEC>(static_cast<IO*>(a.dgate) + at + col, dg);
+        p.store(static_cast<IO*>(a.dgate) + at, i, dg);
       }
-      store_pairs<IO, VEC>(static_cast<IO*>(a.dx) + at + col, d[i]);
+      p.store(static_cast<IO*>(a.dx) + at, i, d[i]);
     }
   }
   float* o = part + ((int64_t)blockIdx.x * p.rows_per_block + p.sub) * 3 * a.width;
 #pragma unroll
   for (int i = 0; i < ITER; ++i)
-    if (p.on(i))
-      for (int c = 0; c < VEC; ++c) {
-        const int col = p.col(i) + c;
-        if (a.dpost) o[col] = c_post[col];
-        if (a.dscale) o[a.width + col] = c_scale[col];
-        if (a.dpre) o[2 * a.width + col] = c_pre[col];
-      }
+#pragma unroll
+    for (int e = 0; e < At::N; ++e)
+      if (p.on(i, e))
+#pragma unroll
+        for (int j = 0; j < UNIT; ++j) {
+          const int c = p.col(i, e) + j;
+          if (a.dpost) o[c] = c_post[c];
+          if (a.dscale) o[a.width + c] = c_scale[c];
+          if (a.dpre) o[2 * a.width + c] = c_pre[c];
+        }
 }
 
 // The backward for wide rows (every thread VEC columns, no gaps): two rows at a
@@ -771,11 +830,11 @@ int resident_blocks(K kernel, int block, int sms, size_t shared) {
   return per * sms;
 }
 
-template <typename IO, typename RT, int VEC, int ITER>
+template <typename IO, typename RT, int VEC, int ITER, int UNIT>
 cudaError_t fwd_launch(const NormArgs& a, const Shape& s, cudaStream_t stream) {
-  auto* k = !a.gate          ? norm_fwd_kernel<IO, RT, VEC, ITER, 0>
-            : !a.gate_first  ? norm_fwd_kernel<IO, RT, VEC, ITER, 1>
-                             : norm_fwd_kernel<IO, RT, VEC, ITER, 2>;
+  auto* k = !a.gate          ? norm_fwd_kernel<IO, RT, VEC, ITER, UNIT, 0>
+            : !a.gate_first  ? norm_fwd_kernel<IO, RT, VEC, ITER, UNIT, 1>
+                             : norm_fwd_kernel<IO, RT, VEC, ITER, UNIT, 2>;
   const int64_t need = (a.tokens * a.heads + s.block / s.tpr - 1) / (s.block / s.tpr);
   const int64_t most = resident_blocks(k, s.block, sm_count(), 0);
   k<<<(unsigned)(need < most ? need : most), s.block, 0, stream>>>(a, s.tpr);
@@ -807,12 +866,12 @@ int64_t bwd_blocks(const NormArgs& a, const Shape& s, int sms) {
   return need < cap ? need : cap;
 }
 
-template <typename IO, typename RT, int VEC, int ITER>
+template <typename IO, typename RT, int VEC, int ITER, int UNIT>
 cudaError_t bwd_launch(const NormArgs& a, const Shape& s, int sms, float* part,
                        cudaStream_t stream) {
-  auto* k = !a.gate          ? norm_bwd_kernel<IO, RT, VEC, ITER, 0>
-            : !a.gate_first  ? norm_bwd_kernel<IO, RT, VEC, ITER, 1>
-                             : norm_bwd_kernel<IO, RT, VEC, ITER, 2>;
+  auto* k = !a.gate          ? norm_bwd_kernel<IO, RT, VEC, ITER, UNIT, 0>
+            : !a.gate_first  ? norm_bwd_kernel<IO, RT, VEC, ITER, UNIT, 1>
+                             : norm_bwd_kernel<IO, RT, VEC, ITER, UNIT, 2>;
   const int per = s.block / s.tpr;
   const int bytes = per * 3 * ((a.width + 3) & ~3) * (int)sizeof(float);
   cudaError_t e = cudaSuccess;
@@ -854,54 +913,74 @@ cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* p
   return cudaGetLastError();
 }
 
-constexpr int kFwd8[] = {4, 1}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8},
-              kOne[] = {4, 32};
+constexpr int kFwd8[] = {4, 1}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8};
+// rows that are not aligned: 16 elements a thread as far as 512 threads go
+constexpr int kOdd8[] = {2, 4}, kOdd4[] = {4, 8};
 
-// 16 bytes of io a load where every pointer, stride and the width allow it,
-// single elements otherwise.
-bool vec_ok(const NormArgs& a, int vec) {
-  const void* io[] = {a.x, a.gate, a.normed, a.d_normed, a.dx, a.dgate,
-                      a.residual, a.out, a.d_out, a.dres};
-  for (const void* p : io)
-    if (p && !aligned_to(p, 16)) return false;
-  return a.width % vec == 0 && a.x_stride % vec == 0 && a.gate_stride % vec == 0;
+// Neighbouring elements an access can take: 16 bytes of io where every
+// pointer, stride and the width allow it, 2 elements where they allow that.
+int unit_of(const NormArgs& a) {
+  const int vec = a.bf16 ? 8 : 4;
+  const void* io[] = {a.x, a.gate, a.normed, a.d_normed, a.dx, a.dgate};
+  const void* res[] = {a.residual, a.out, a.d_out, a.dres};
+  for (const int u : {vec, 2}) {
+    const size_t e = a.bf16 ? 2 : 4, r = a.res_bf16 ? 2 : 4;
+    bool ok = a.width % u == 0 && a.x_stride % u == 0 && a.gate_stride % u == 0;
+    for (const void* p : io) ok = ok && aligned_to(p, u * e);
+    for (const void* p : res) ok = ok && aligned_to(p, u * r > 16 ? 16 : u * r);
+    if (ok) return u;
+  }
+  return 1;
 }
 
-Shape bwd_shape(const NormArgs& a, bool vec) {
-  if (!vec) return row_shape(a, 1, kOne, 2);
-  return a.bf16 ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 4, kBwd4, 4);
+Shape shape_of(const NormArgs& a, bool bwd, int unit) {
+  if (a.bf16)
+    return unit < 8 ? row_shape(a, 8, kOdd8, 2)
+                    : bwd ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 8, kFwd8, 2);
+  return unit < 4 ? row_shape(a, 4, kOdd4, 2)
+                  : bwd ? row_shape(a, 4, kBwd4, 4) : row_shape(a, 4, kFwd4, 3);
 }
 
-template <typename IO, typename RT, int VEC>
+template <typename IO, typename RT, int VEC, int UNIT>
 cudaError_t fwd_pick(const NormArgs& a, cudaStream_t st) {
-  if constexpr (VEC > 1) {
-    const Shape s = VEC == 8 ? row_shape(a, 8, kFwd8, 2) : row_shape(a, 4, kFwd4, 3);
-    if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1>(a, s, st);
-    if (s.iter == 4) return fwd_launch<IO, RT, VEC, 4>(a, s, st);
-    if constexpr (VEC == 4) return fwd_launch<IO, RT, VEC, 8>(a, s, st);
-    return cudaErrorInvalidValue;
-  } else {
-    const Shape s = row_shape(a, 1, kOne, 2);
-    if (s.iter == 4) return fwd_launch<IO, RT, 1, 4>(a, s, st);
-    return fwd_launch<IO, RT, 1, 32>(a, s, st);
-  }
+  const Shape s = shape_of(a, false, UNIT);
+  if constexpr (UNIT == VEC)
+    if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1, UNIT>(a, s, st);
+  if constexpr (UNIT < VEC && VEC == 8)
+    if (s.iter == 2) return fwd_launch<IO, RT, VEC, 2, UNIT>(a, s, st);
+  if (s.iter == 4) return fwd_launch<IO, RT, VEC, 4, UNIT>(a, s, st);
+  if constexpr (VEC == 4)
+    if (s.iter == 8) return fwd_launch<IO, RT, VEC, 8, UNIT>(a, s, st);
+  return cudaErrorInvalidValue;
+}
+template <typename IO, typename RT, int VEC>
+cudaError_t fwd_unit(const NormArgs& a, cudaStream_t st) {
+  const int u = unit_of(a);
+  return u == VEC ? fwd_pick<IO, RT, VEC, VEC>(a, st)
+         : u == 2 ? fwd_pick<IO, RT, VEC, 2>(a, st)
+                  : fwd_pick<IO, RT, VEC, 1>(a, st);
 }
 
-template <typename IO, typename RT, int VEC>
+template <typename IO, typename RT, int VEC, int UNIT>
 cudaError_t bwd_pick(const NormArgs& a, int sms, float* part, cudaStream_t st) {
-  const Shape s = bwd_shape(a, VEC > 1);
-  if constexpr (VEC > 1) {
-    if (const PairShape q = pair_shape(a, VEC); q.threads)
-      return pair_launch<IO, RT, VEC>(a, q, sms, part, st);
-    if (s.iter == 1) return bwd_launch<IO, RT, VEC, 1>(a, s, sms, part, st);
-    if (s.iter == 2) return bwd_launch<IO, RT, VEC, 2>(a, s, sms, part, st);
-    if (s.iter == 4) return bwd_launch<IO, RT, VEC, 4>(a, s, sms, part, st);
-    if constexpr (VEC == 4) return bwd_launch<IO, RT, VEC, 8>(a, s, sms, part, st);
-    return cudaErrorInvalidValue;
-  } else {
-    if (s.iter == 4) return bwd_launch<IO, RT, 1, 4>(a, s, sms, part, st);
-    return bwd_launch<IO, RT, 1, 32>(a, s, sms, part, st);
-  }
+  const Shape s = shape_of(a, true, UNIT);
+  if constexpr (UNIT == VEC)
+    if (s.iter == 1) return bwd_launch<IO, RT, VEC, 1, UNIT>(a, s, sms, part, st);
+  if constexpr (UNIT == VEC || VEC == 8)
+    if (s.iter == 2) return bwd_launch<IO, RT, VEC, 2, UNIT>(a, s, sms, part, st);
+  if (s.iter == 4) return bwd_launch<IO, RT, VEC, 4, UNIT>(a, s, sms, part, st);
+  if constexpr (VEC == 4)
+    if (s.iter == 8) return bwd_launch<IO, RT, VEC, 8, UNIT>(a, s, sms, part, st);
+  return cudaErrorInvalidValue;
+}
+template <typename IO, typename RT, int VEC>
+cudaError_t bwd_unit(const NormArgs& a, int sms, float* part, cudaStream_t st) {
+  const int u = unit_of(a);
+  if (const PairShape q = pair_shape(a, u == VEC ? VEC : 1); q.threads)
+    return pair_launch<IO, RT, VEC>(a, q, sms, part, st);
+  return u == VEC ? bwd_pick<IO, RT, VEC, VEC>(a, sms, part, st)
+         : u == 2 ? bwd_pick<IO, RT, VEC, 2>(a, sms, part, st)
+                  : bwd_pick<IO, RT, VEC, 1>(a, sms, part, st);
 }
 
 }  // namespace
@@ -909,35 +988,29 @@ cudaError_t bwd_pick(const NormArgs& a, int sms, float* part, cudaStream_t st) {
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   if (a.tokens == 0) return cudaSuccess;
   using bf = __nv_bfloat16;
-  if (a.bf16 && a.res_bf16)
-    return vec_ok(a, 8) ? fwd_pick<bf, bf, 8>(a, st) : fwd_pick<bf, bf, 1>(a, st);
-  if (a.bf16) return vec_ok(a, 8) ? fwd_pick<bf, float, 8>(a, st) : fwd_pick<bf, float, 1>(a, st);
-  return vec_ok(a, 4) ? fwd_pick<float, float, 4>(a, st) : fwd_pick<float, float, 1>(a, st);
+  return a.bf16 && a.res_bf16 ? fwd_unit<bf, bf, 8>(a, st)
+         : a.bf16             ? fwd_unit<bf, float, 8>(a, st)
+                              : fwd_unit<float, float, 4>(a, st);
 }
 
 size_t norm_bwd_workspace_bytes(const NormArgs& a, int sms) {
   if (!a.dpost && !a.dscale && !a.dpre) return 0;
-  const bool vec = vec_ok(a, a.bf16 ? 8 : 4);
-  if (const PairShape q = pair_shape(a, vec ? (a.bf16 ? 8 : 4) : 1); q.threads) {
+  const int vec = a.bf16 ? 8 : 4, unit = unit_of(a);
+  if (const PairShape q = pair_shape(a, unit == vec ? vec : 1); q.threads) {
     const int64_t need = (a.tokens * a.heads + kPairRows - 1) / kPairRows,
                   cap = (int64_t)sms * (1024 / q.threads);
     return (size_t)(need < cap ? need : cap) * 3 * a.width * sizeof(float);
   }
-  const Shape s = bwd_shape(a, vec);
+  const Shape s = shape_of(a, true, unit);
   return (size_t)bwd_blocks(a, s, sms) * (s.block / s.tpr) * 3 * a.width * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, void* ws, int sms, cudaStream_t st) {
   using bf = __nv_bfloat16;
   float* part = static_cast<float*>(ws);
-  if (a.bf16 && a.res_bf16)
-    return vec_ok(a, 8) ? bwd_pick<bf, bf, 8>(a, sms, part, st)
-                        : bwd_pick<bf, bf, 1>(a, sms, part, st);
-  if (a.bf16)
-    return vec_ok(a, 8) ? bwd_pick<bf, float, 8>(a, sms, part, st)
-                        : bwd_pick<bf, float, 1>(a, sms, part, st);
-  return vec_ok(a, 4) ? bwd_pick<float, float, 4>(a, sms, part, st)
-                      : bwd_pick<float, float, 1>(a, sms, part, st);
+  return a.bf16 && a.res_bf16 ? bwd_unit<bf, bf, 8>(a, sms, part, st)
+         : a.bf16             ? bwd_unit<bf, float, 8>(a, sms, part, st)
+                              : bwd_unit<float, float, 4>(a, sms, part, st);
 }
 
 }  // namespace kda
