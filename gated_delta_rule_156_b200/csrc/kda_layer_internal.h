@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kda {
 
 enum Act { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
@@ -15,12 +17,16 @@ enum Act { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
 cudaError_t api_take_workspace(size_t bytes, cudaStream_t stream, void** ws);
 void api_record_cuda_error(cudaError_t e);
 
-// SM count of the current device.
+// SM count of the current device (looked up once per device).
 inline int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
     return 148;
+  known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

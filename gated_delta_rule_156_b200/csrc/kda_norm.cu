@@ -821,12 +821,27 @@ Shape row_shape(const NormArgs& a, int vec, const int* iters, int n) {
   return best;
 }
 
+// Resident blocks of a launch on the whole device.  Every device that this
+// library serves is the same chip, so what the runtime said for a kernel is
+// remembered for the thread's next calls.
 template <typename K>
 int resident_blocks(K kernel, int block, int sms, size_t shared) {
+  struct Known {
+    const void* kernel;
+    int block, per;
+    size_t shared;
+  };
+  static thread_local Known known[8];
+  static thread_local int next = 0;
+  const void* key = reinterpret_cast<const void*>(kernel);
+  for (const Known& k : known)
+    if (k.kernel == key && k.block == block && k.shared == shared) return k.per * sms;
   int per = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, shared) != cudaSuccess ||
       per < 1)
-    per = 1;
+    return sms;
+  known[next] = Known{key, block, per, shared};
+  next = (next + 1) % 8;
   return per * sms;
 }
 

@@ -490,24 +490,32 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
   if (ENDS && on && l == 0) split.steps[id * a.D + d] = steps;
 }
 
-// dB and dC of a token's group: the channel blocks' parts.
-template <typename IO>
-__global__ void ssm_bc_sum_kernel(SsmBwdArgs b, const float* __restrict__ bc, int blocks_per_group) {
+// dB and dC of a token's group: the channel blocks' parts, N values a thread.
+template <typename IO, int N>
+__global__ void __launch_bounds__(256)
+    ssm_bc_sum_kernel(SsmBwdArgs b, const float* __restrict__ bc, int blocks_per_group) {
   const SsmArgs& a = b.f;
-  const int64_t per = (int64_t)2 * a.S;
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= a.tokens * a.G * per) return;
-  const int e = (int)(id % per);
-  const int64_t tg = id / per;
-  const int g = (int)(tg % a.G);
+  const int per = 2 * a.S / N;  // threads a token and group
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, tg = id / per;
+  const int e = (int)(id - tg * per) * N;
   const int64_t tok = tg / a.G;
+  const int g = (int)(tg - tok * a.G);
+  if (tok >= a.tokens) return;
   SeqCursor q;
   if (!find_seq(a.cu, a.n_seqs, a.T, (int)tok, &q) || tok < q.start) return;
-  float s = 0.f;
-  for (int i = 0; i < blocks_per_group; ++i)
-    s += bc[((int64_t)(g * blocks_per_group + i) * a.tokens + tok) * per + e];
-  IO* out = static_cast<IO*>(e < a.S ? b.dB : b.dC);
-  out[(tok * a.G + g) * a.S + e % a.S] = from_f32<IO>(s);
+  const int64_t step = a.tokens * 2 * a.S;
+  const float* p = bc + g * blocks_per_group * step + tok * 2 * a.S + e;
+  float s[N] = {};
+#pragma unroll 8
+  for (int i = 0; i < blocks_per_group; ++i) {
+    float v[N];
+    load_vec<float, N>(p + i * step, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] += v[j];
+  }
+  IO* out = static_cast<IO*>(e < a.S ? b.dB : b.dC) + (tok * a.G + g) * a.S + e % a.S;
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = from_f32<IO>(s[j]);
 }
 
 // dA, dskip and dbias: the segments' parts, 8 rows of threads and then their
@@ -607,7 +615,10 @@ cudaError_t bwd_pick(const SsmBwdArgs& b, const BwdParts& part, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const int64_t n = b.f.tokens * b.f.G * 2 * b.f.S;
   const int per_group = ssm_blocks(b.f, kSsmThreads / ssm_lanes(b.f.S)) / b.f.G;
-  if (n) ssm_bc_sum_kernel<IO><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(b, part.bc, per_group);
+  if (n && b.f.S % 4 == 0)
+    ssm_bc_sum_kernel<IO, 4><<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(b, part.bc, per_group);
+  else if (n)
+    ssm_bc_sum_kernel<IO, 1><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(b, part.bc, per_group);
   return cudaGetLastError();
 }
 

@@ -724,6 +724,11 @@ def _sequences(x, dev, cu_seqlens):
     return n, n
 
 
+def _empty(t):
+    """An uninitialised dense tensor of t's shape and dtype."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _run(name, shape, tensors, stream):
     st = getattr(library(), name)(
         ctypes.byref(shape),
@@ -765,7 +770,7 @@ def short_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None,
     _need("out", out, dev, dt, full, optional=True)
     with _On(dev, stream) as s:
         if out is None:
-            out = x.new_empty(full)
+            out = _empty(x)
         final = x.new_empty(state) if want_final_state else None
         _run("kda_short_conv_fwd", shape,
              (x, weight, bias, initial_state, cu_seqlens, out, final), s)
@@ -784,7 +789,7 @@ def short_conv_bwd(x, weight, bias, initial_state, cu_seqlens, d_out,
     _need("d_out", d_out, dev, dt, full)
     _need("d_final_state", d_final_state, dev, dt, state, optional=True)
     with _On(dev, stream) as s:
-        dx = x.new_empty(full)
+        dx = _empty(x)
         dw = torch.empty_like(weight)
         db = None if bias is None else torch.empty_like(bias)
         d0 = x.new_empty(state) if want_initial_state else None
@@ -804,7 +809,7 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None,
     _need("out", out, dev, dt, full, optional=True)
     with _On(dev, stream) as s:
         if out is None:
-            out = x.new_empty(full)
+            out = _empty(x)
         _run("kda_short_conv_step", shape, (x, weight, bias, state, out), s)
     return out
 
@@ -851,7 +856,7 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
     _need("final_state", final_state, dev, f32, state, optional=True)
     with _On(dev, stream) as s:
         if out is None:
-            out = u.new_empty(full)
+            out = _empty(u)
         if final_state is None:
             final_state = A.new_empty(state)
         _run("kda_ssm_scan_fwd", shape,
@@ -874,11 +879,11 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
     _need("d_out", d_out, dev, dt, full)
     _need("d_final_state", d_final_state, dev, f32, state, optional=True)
     with _On(dev, stream) as s:
-        du, dd = u.new_empty(full), u.new_empty(full)
+        du, dd = _empty(u), _empty(u)
         dA = torch.empty_like(A)
-        dB, dC = u.new_empty(Bm.shape), u.new_empty(Bm.shape)
+        dB, dC = _empty(Bm), _empty(Bm)
         dD = None if D is None else torch.empty_like(D)
-        dz = None if z is None else u.new_empty(full)
+        dz = None if z is None else _empty(u)
         db = None if delta_bias is None else torch.empty_like(delta_bias)
         d0 = A.new_empty(state) if want_initial_state else None
         _run("kda_ssm_scan_bwd", shape,
@@ -912,7 +917,7 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None,
     _need("out", out, dev, dt, full, optional=True)
     with _On(dev, stream) as s:
         if out is None:
-            out = u.new_empty(full)
+            out = _empty(u)
         _run("kda_ssm_step", shape,
              (u, delta, A, Bm, Cm, D, z, delta_bias, state, out), s)
     return out
@@ -973,9 +978,9 @@ def block_norm_fwd(x, post_weight=None, gate=None, residual=None, scale=None,
     _need("normed", normed, dev, dt, x.shape, optional=True)
     with _On(dev, stream) as s:
         if out is None:
-            out = x.new_empty(x.shape, dtype=rt)
+            out = _empty(x if residual is None else residual)
         if normed is None and pre_weight is not None:
-            normed = x.new_empty(x.shape)
+            normed = _empty(x)
         _run("kda_block_norm_fwd", shape,
              (x, post_weight, gate, residual, scale, pre_weight, out, normed),
              s)
@@ -998,13 +1003,11 @@ def block_norm_bwd(x, post_weight=None, gate=None, residual=None, scale=None,
     _need("d_out", d_out, dev, rt, x.shape, optional=True)
     _need("d_normed", d_normed, dev, dt, x.shape, optional=True)
 
-    def like(t, dtype):
-        return None if t is None else x.new_empty(t.shape, dtype=dtype)
+    def like(t):
+        return None if t is None else _empty(t)
     with _On(dev, stream) as s:
-        dx, dg, dr = like(x, dt), like(gate, dt), like(residual, rt)
-        f32 = torch.float32
-        dpost, dscale, dpre = (like(t, f32) for t in
-                               (post_weight, scale, pre_weight))
+        dx, dg, dr = like(x), like(gate), like(residual)
+        dpost, dscale, dpre = like(post_weight), like(scale), like(pre_weight)
         _run("kda_block_norm_bwd", shape,
              (x, post_weight, gate, residual, scale, pre_weight, d_out,
               d_normed, dx, dg, dr, dpost, dscale, dpre), s)
