@@ -67,10 +67,12 @@ kda_status check_memory(const Span* in, int n_in, const Span* out, int n_out) {
 size_t elem(kda_dtype t) { return t == KDA_BF16 ? 2 : 4; }
 bool dtype_ok(int t) { return t == KDA_BF16 || t == KDA_F32; }
 
-// A token stride: 0 is dense; tokens must not overlap.
+// A token stride: 0 is dense; tokens must not overlap.  Below 2^30 elements, so
+// that 2^31 tokens of them are counted in 64 bits.
+constexpr int64_t kMaxStride = (int64_t)1 << 30;
 bool stride_of(int64_t given, int64_t width, int64_t* s) {
   *s = given ? given : width;
-  return *s >= width && *s <= ((int64_t)1 << 40);
+  return *s >= width && *s <= kMaxStride;
 }
 
 // B, T, n_seqs of a dense or packed batch.
@@ -122,8 +124,8 @@ kda_status ssm_args(const kda_ssm_shape* s, bool packed, kda::SsmArgs* a) {
   a->softplus = s->softplus != 0;
   a->b_group = s->b_group_stride ? s->b_group_stride : s->S;
   a->c_group = s->c_group_stride ? s->c_group_stride : s->S;
-  if (a->b_group < s->S || a->c_group < s->S || a->b_group > (1 << 30) ||
-      a->c_group > (1 << 30))
+  if (a->b_group < s->S || a->c_group < s->S || a->b_group > kMaxStride ||
+      a->c_group > kMaxStride)
     return KDA_ERR_INVALID_ARG;
   if (!stride_of(s->u_stride, s->D, &a->u_stride) ||
       !stride_of(s->delta_stride, s->D, &a->delta_stride) ||
@@ -133,8 +135,8 @@ kda_status ssm_args(const kda_ssm_shape* s, bool packed, kda::SsmArgs* a) {
   const int64_t bw = (s->G - 1) * a->b_group + s->S, cw = (s->G - 1) * a->c_group + s->S;
   a->b_stride = s->b_stride ? s->b_stride : (int64_t)s->G * a->b_group;
   a->c_stride = s->c_stride ? s->c_stride : (int64_t)s->G * a->c_group;
-  if (a->b_stride < bw || a->c_stride < cw || a->b_stride > ((int64_t)1 << 40) ||
-      a->c_stride > ((int64_t)1 << 40))
+  if (a->b_stride < bw || a->c_stride < cw || a->b_stride > kMaxStride ||
+      a->c_stride > kMaxStride)
     return KDA_ERR_INVALID_ARG;
   // CTAs (of segments of 128 tokens at the least, where a scan is split) and
   // the backward's sums are counted in 31 bits
@@ -176,7 +178,7 @@ kda_status norm_args(const kda_norm_shape* s, kda::NormArgs* a) {
   if (s->width > 16384 || s->heads > 65535) return KDA_ERR_UNSUPPORTED;
   if (s->io_dtype == KDA_F32 && s->residual_dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
   const int64_t w = (int64_t)s->heads * s->width;
-  if (s->tokens > ((int64_t)1 << 40) / w) return KDA_ERR_UNSUPPORTED;
+  if (s->tokens > INT32_MAX || w > kMaxStride) return KDA_ERR_UNSUPPORTED;
   if (!stride_of(s->x_stride, w, &a->x_stride) || !stride_of(s->gate_stride, w, &a->gate_stride))
     return KDA_ERR_INVALID_ARG;
   a->tokens = s->tokens;

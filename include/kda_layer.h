@@ -14,7 +14,7 @@
  * Layouts are token-major and row-major.  Tensors marked "token stride" may
  * be slices of a wider projection output: the elements of one token are
  * consecutive, and consecutive tokens of the flat [B * T] axis are
- * `*_stride` elements apart (0: dense).  Every tensor must be aligned to its
+ * `*_stride` elements apart (0: dense; at most 2^30).  Every tensor must be aligned to its
  * element (KDA_ERR_MISALIGNED otherwise); 16-byte aligned pointers and
  * strides take the wide loads.
  *
@@ -229,7 +229,7 @@ KDA_API kda_status kda_block_norm_fwd(
  * d_residual (residual dtype, only with residual), all dense; d_post_weight,
  * d_scale, d_pre_weight [width] fp32, each only with its input.  The sums over
  * rows are fp32 in a fixed order: repeats are bit-identical.  Stream-ordered
- * workspace of up to 3 * width floats per resident block.
+ * workspace of up to 3 * width floats for each row in work on the device.
  */
 KDA_API kda_status kda_block_norm_bwd(
     const kda_norm_shape* shape, const void* x, const float* post_weight,

@@ -79,7 +79,8 @@ def test_conv(lib, name, names, step):
     assert c(None) == INV
     for bad in (dict(T=-1), dict(B=-1), dict(D=0), dict(io_dtype=5),
                 dict(activation=2), dict(activation=-1), dict(x_stride=63),
-                dict(x_stride=-64)):
+                dict(x_stride=-64), dict(x_stride=1 << 40),
+                dict(x_stride=2 ** 62)):
         assert c(conv(**bad)) == INV, bad
     for bad in (dict(W=1), dict(W=5), dict(D=(1 << 20) + 1),
                 dict(T=2 ** 31 - 1)):
@@ -119,7 +120,9 @@ def test_ssm(lib, name, names, step):
                 dict(io_dtype=2), dict(u_stride=63), dict(delta_stride=1),
                 dict(z_stride=-1), dict(b_group_stride=15),
                 dict(b_stride=31), dict(c_stride=31),
-                dict(c_group_stride=20, c_stride=32)):
+                dict(c_group_stride=20, c_stride=32),
+                dict(u_stride=1 << 40), dict(b_stride=2 ** 62),
+                dict(c_group_stride=2 ** 62)):
         assert c(ssm(**bad)) == INV, bad
     for bad in (dict(S=129), dict(D=1 << 21), dict(T=2 ** 31 - 1)):
         assert c(ssm(**bad)) == UNS, bad
@@ -158,9 +161,11 @@ def test_norm(lib, name, names):
     for bad in (dict(tokens=-1), dict(heads=0), dict(width=0),
                 dict(io_dtype=9), dict(residual_dtype=2), dict(gate_act=3),
                 dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
-                dict(x_stride=127), dict(gate_stride=-128)):
+                dict(x_stride=127), dict(gate_stride=-128),
+                dict(x_stride=1 << 40)):
         assert c(norm(**bad)) == INV, bad
-    for bad in (dict(width=16385), dict(io_dtype=1, residual_dtype=0)):
+    for bad in (dict(width=16385), dict(io_dtype=1, residual_dtype=0),
+                dict(tokens=1 << 40), dict(heads=65536)):
         assert c(norm(**bad)) == UNS, bad
     assert c(norm(), x=None) == INV
     assert c(norm(), x=BASE + GAP + 1) == MIS
