@@ -15,7 +15,39 @@ namespace kda {
 
 namespace {
 
-constexpr int kUnroll = 4;  // token loads in flight per thread
+// Tokens on their way: a ring of kStages groups of kGroup tokens in shared
+// memory, filled by asynchronous copies.  A thread copies just what it will
+// read itself (no barrier), and three groups in flight cost it no registers
+// (2 x 8192 x 4096 forward: 55 us, 63 with the next group in registers).
+// Vectors of 4 elements; single elements are loaded 8 tokens at a time.
+constexpr int kGroup = 4, kStages = 4;
+template <typename IO, int VEC>
+struct Ring {
+  static constexpr int BYTES = VEC * (int)sizeof(IO);
+  static constexpr bool ON = BYTES >= 8;
+  unsigned char* at;  // this thread's first vector
+  int step;           // to its next one
+  __device__ __forceinline__ Ring(unsigned char* base, int tid, int threads)
+      : at(base + tid * BYTES), step(threads * BYTES) {}
+  // vector i of a group of `arrays` * kGroup vectors
+  __device__ __forceinline__ unsigned char* place(int stage, int n, int i) const {
+    return at + (stage * n + i) * step;
+  }
+  __device__ __forceinline__ static void send(unsigned char* to, const IO* from) {
+    const unsigned dst = (unsigned)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from));
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(from));
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;"); }
+  __device__ __forceinline__ static void wait() {  // for the oldest group in flight
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+  }
+  __device__ __forceinline__ static Raw<IO, VEC> take(const unsigned char* from) {
+    return *reinterpret_cast<const Raw<IO, VEC>*>(from);
+  }
+};
 
 // A thread's channels go in pairs through the packed fp32 arithmetic.
 template <typename IO, int W, int VEC>
@@ -102,9 +134,12 @@ __device__ __forceinline__ void slide(f32x2 (&win)[W - 1][P], const f32x2 (&x)[P
 // Block (channel vectors, runs); the grid's runs go over all tokens, then
 // over the n_seqs * (W - 1) rows of the final states.
 template <typename IO, int W, int VEC>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 4)
     conv_fwd_kernel(ConvArgs a, int nvec, int run, int64_t n_runs) {
   constexpr int P = kPairs<VEC>;
+  using R = Ring<IO, VEC>;
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  const R ring(s_ring, threadIdx.y * blockDim.x + threadIdx.x, 256);
   const int cv = blockIdx.y * blockDim.x + threadIdx.x;
   int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (cv >= nvec) return;
@@ -148,23 +183,34 @@ __global__ void __launch_bounds__(256, 3)
       slide<W>(win, v);
       po += a.D;
     };
-    // groups of tokens; the next group's loads go out before this one's work
     int left = (int)(e - t);
-    Raw<IO, VEC> raw[2][kUnroll];
-    auto fetch = [&](Raw<IO, VEC>(&r)[kUnroll]) {
+    if constexpr (R::ON) {
+      const int groups = left / kGroup;
+      auto fetch = [&](int n) {
+        if (n < groups)
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) r[i] = load_raw<IO, VEC>(px + i * a.x_stride);
-      px += kUnroll * a.x_stride;
-    };
-    if (left >= kUnroll) fetch(raw[0]);
-    while (left >= kUnroll) {
+          for (int i = 0; i < kGroup; ++i)
+            R::send(ring.place(n % kStages, kGroup, i), px + (n * kGroup + i) * a.x_stride);
+        R::commit();
+      };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (left < kUnroll) break;
-        left -= kUnroll;
-        if (left >= kUnroll) fetch(raw[h ^ 1]);
+      for (int n = 0; n < kStages - 1; ++n) fetch(n);
+      for (int n = 0; n < groups; ++n) {
+        R::wait();
+        fetch(n + kStages - 1);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) token(raw[h][i]);
+        for (int i = 0; i < kGroup; ++i) token(R::take(ring.place(n % kStages, kGroup, i)));
+      }
+      px += groups * kGroup * a.x_stride;
+      left -= groups * kGroup;
+    } else {
+      for (; left >= 2 * kGroup; left -= 2 * kGroup) {
+        Raw<IO, VEC> raw[2 * kGroup];
+#pragma unroll
+        for (int i = 0; i < 2 * kGroup; ++i) raw[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+        px += 2 * kGroup * a.x_stride;
+#pragma unroll
+        for (int i = 0; i < 2 * kGroup; ++i) token(raw[i]);
       }
     }
     for (; left > 0; --left) {
@@ -181,7 +227,7 @@ __global__ void __launch_bounds__(256, 3)
 // and db over the run itself.  The block's runs are summed in shared memory
 // in a fixed order; conv_weight_sum_kernel sums the blocks.  The rows of
 // d_initial_state are independent of the runs and have threads of their own.
-constexpr int kBwdLanes = 32, kBwdRuns = 8, kBwdUnroll = 4;
+constexpr int kBwdLanes = 32, kBwdRuns = 8;
 
 template <typename IO, int W, int VEC>
 __device__ void past_grad(const ConvArgs& a, const Taps<IO, W, VEC>& k, int64_t row,
@@ -226,6 +272,9 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns, 2)
     conv_bwd_kernel(ConvArgs a, int nvec, int run, int64_t n_blocks,
                     float* __restrict__ part) {
   __shared__ float s_part[kBwdRuns][W + 1][kBwdLanes][VEC];
+  using R = Ring<IO, VEC>;
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  const R ring(s_ring, threadIdx.y * kBwdLanes + threadIdx.x, kBwdLanes * kBwdRuns);
   const int cv = blockIdx.y * kBwdLanes + threadIdx.x;
   const bool on = cv < nvec;
   const int c0 = on ? cv * VEC : 0;
@@ -293,27 +342,44 @@ __global__ void __launch_bounds__(kBwdLanes* kBwdRuns, 2)
       po += a.D;
       slide<W>(win, xv);
     };
-    // groups of tokens; the next group's loads go out before this one's work
     int left = (int)(e - t);
-    Raw<IO, VEC> rx[2][kBwdUnroll], ry[2][kBwdUnroll];
-    auto fetch = [&](Raw<IO, VEC>(&qx)[kBwdUnroll], Raw<IO, VEC>(&qy)[kBwdUnroll]) {
+    if constexpr (R::ON) {
+      const int groups = left / kGroup;
+      auto fetch = [&](int n) {
+        if (n < groups)
 #pragma unroll
-      for (int i = 0; i < kBwdUnroll; ++i) {
-        qx[i] = load_raw<IO, VEC>(px + i * a.x_stride);
-        qy[i] = load_raw<IO, VEC>(py + i * (int64_t)a.D);
+          for (int i = 0; i < kGroup; ++i) {
+            R::send(ring.place(n % kStages, 2 * kGroup, i), px + (n * kGroup + i) * a.x_stride);
+            R::send(ring.place(n % kStages, 2 * kGroup, kGroup + i),
+                    py + (n * kGroup + i) * (int64_t)a.D);
+          }
+        R::commit();
+      };
+#pragma unroll
+      for (int n = 0; n < kStages - 1; ++n) fetch(n);
+      for (int n = 0; n < groups; ++n) {
+        R::wait();
+        fetch(n + kStages - 1);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+          token(R::take(ring.place(n % kStages, 2 * kGroup, i)),
+                R::take(ring.place(n % kStages, 2 * kGroup, kGroup + i)), true);
       }
-      px += kBwdUnroll * a.x_stride;
-      py += kBwdUnroll * (int64_t)a.D;
-    };
-    if (left >= kBwdUnroll) fetch(rx[0], ry[0]);
-    while (left >= kBwdUnroll) {
+      px += groups * kGroup * a.x_stride;
+      py += groups * kGroup * (int64_t)a.D;
+      left -= groups * kGroup;
+    } else {
+      for (; left >= 2 * kGroup; left -= 2 * kGroup) {
+        Raw<IO, VEC> rx[2 * kGroup], ry[2 * kGroup];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (left < kBwdUnroll) break;
-        left -= kBwdUnroll;
-        if (left >= kBwdUnroll) fetch(rx[h ^ 1], ry[h ^ 1]);
+        for (int i = 0; i < 2 * kGroup; ++i) {
+          rx[i] = load_raw<IO, VEC>(px + i * a.x_stride);
+          ry[i] = load_raw<IO, VEC>(py + i * (int64_t)a.D);
+        }
+        px += 2 * kGroup * a.x_stride;
+        py += 2 * kGroup * (int64_t)a.D;
 #pragma unroll
-        for (int i = 0; i < kBwdUnroll; ++i) token(rx[h][i], ry[h][i], true);
+        for (int i = 0; i < 2 * kGroup; ++i) token(rx[i], ry[i], true);
       }
     }
     for (int i = left + (int)(stop - e); i > 0; --i) {
@@ -435,6 +501,12 @@ dim3 block_shape(int nvec) {
   return dim3(lx, 256 / lx);
 }
 
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes) {
+  if (bytes <= 24 * 1024) return cudaSuccess;  // static shared memory comes on top
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 bool vec_ok(const ConvArgs& a, int vec, size_t bytes) {
   const void* ps[] = {a.x, a.past, a.out, a.final_state, a.d_out, a.d_final, a.dx, a.d_past};
   for (const void* p : ps)
@@ -453,7 +525,11 @@ cudaError_t fwd_launch(const ConvArgs& a, cudaStream_t stream) {
   const int64_t n_runs = (a.tokens + run - 1) / run;
   const int64_t rows = n_runs + (a.final_state ? (int64_t)a.n_seqs * (W - 1) : 0);
   const dim3 grid((unsigned)((rows + block.y - 1) / block.y), (nvec + block.x - 1) / block.x);
-  if (rows) conv_fwd_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec, run, n_runs);
+  constexpr int bytes = Ring<IO, VEC>::ON ? kStages * kGroup * 256 * Ring<IO, VEC>::BYTES : 0;
+  auto* k = conv_fwd_kernel<IO, W, VEC>;
+  const cudaError_t e = allow_shared(k, bytes);
+  if (e != cudaSuccess) return e;
+  if (rows) k<<<grid, block, bytes, stream>>>(a, nvec, run, n_runs);
   return cudaGetLastError();
 }
 
@@ -472,9 +548,17 @@ cudaError_t step_launch(const ConvArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-constexpr int kBwdRun = 32;
+// Tokens a thread takes backward: 64 (which reads 3 of 67 again and sums 512
+// tokens before a part is written), fewer where that would not give every SM
+// its two blocks.
+int bwd_run(const ConvArgs& a) {
+  int run = 64;
+  while (run > 8 && a.tokens / run * (a.D / 4) < (int64_t)148 * 512) run /= 2;
+  return run;
+}
 int64_t bwd_blocks(const ConvArgs& a) {
-  return (a.tokens + kBwdRun * kBwdRuns - 1) / (kBwdRun * kBwdRuns);
+  const int64_t per = (int64_t)bwd_run(a) * kBwdRuns;
+  return (a.tokens + per - 1) / per;
 }
 
 template <typename IO, int W, int VEC>
@@ -485,10 +569,12 @@ cudaError_t bwd_launch(const ConvArgs& a, float* part, cudaStream_t stream) {
   const dim3 block(kBwdLanes, kBwdRuns);
   const dim3 grid((unsigned)(blocks + (rows + kBwdRuns - 1) / kBwdRuns),
                   (nvec + kBwdLanes - 1) / kBwdLanes);
-  if (grid.x)
-    conv_bwd_kernel<IO, W, VEC><<<grid, block, 0, stream>>>(a, nvec, kBwdRun, blocks, part);
-  cudaError_t e = cudaGetLastError();
+  constexpr int bytes = Ring<IO, VEC>::ON ? kStages * 2 * kGroup * 256 * Ring<IO, VEC>::BYTES : 0;
+  auto* k = conv_bwd_kernel<IO, W, VEC>;
+  cudaError_t e = allow_shared(k, bytes);
   if (e != cudaSuccess) return e;
+  if (grid.x) k<<<grid, block, bytes, stream>>>(a, nvec, bwd_run(a), blocks, part);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   conv_weight_sum_kernel<<<dim3((a.D + 31) / 32, W + 1), dim3(32, 8), 0, stream>>>(
       part, blocks, W, a.D, a.dw, a.db);
   return cudaGetLastError();

@@ -83,7 +83,8 @@ KDA_API kda_status kda_short_conv_fwd(const kda_conv_shape* shape,
  * dtype, dense.  Writes dx [B, T, D] io dtype; d_weight [D, W] and d_bias [D]
  * fp32 (d_bias may be NULL); d_initial_state [N, W-1, D] io dtype or NULL.
  * The weights' sums over tokens are fp32 in a fixed order: repeats are
- * bit-identical.  Stream-ordered workspace of (W + 1) D floats per 256 tokens.
+ * bit-identical.  Stream-ordered workspace of at most (W + 1) D floats for
+ * each 64 tokens (512 in large calls).
  */
 KDA_API kda_status kda_short_conv_bwd(
     const kda_conv_shape* shape, const void* x, const float* weight,
