@@ -11,8 +11,8 @@
 // HBM is the bound; to reach it, a row's fixed cost (its sums over threads, its
 // addresses) must be spread over many elements a thread.  Work split: TPR
 // threads own a row (part of a warp for a head's row, a block for a wide one)
-// with up to 32 elements a thread forward, 16 backward, and several blocks an
-// SM, so that one row's loads run under another's sums.  (With 8 elements a
+// with 16 elements a thread (32 in the widest rows), and several blocks an SM,
+// so that one row's loads run under another's sums.  (With 8 elements a
 // thread and one or two blocks an SM, rows prefetched through registers or an
 // asynchronous ring included, 16384 x 4096 took 0.21 to 0.33 ms.)  Each thread
 // meets the same elements of every row, so the weights' gradients are sums of
@@ -68,18 +68,33 @@ struct RowSum {
     if ((threadIdx.x & 31) == 0)
       s[threadIdx.x >> 5] = make_float4(v[0], v[1 % N], v[2 % N], v[3 % N]);
     __syncthreads();
-    float4 t = s[0];
-    for (int i = 1; i < tpr >> 5; ++i) {
-      const float4 u = s[i];
-      t.x += u.x;
-      if (N > 1) t.y += u.y;
-      if (N > 2) t.z += u.z;
-      if (N > 3) t.w += u.w;
+    const int warps = tpr >> 5;
+    if (warps <= 4) {
+      float4 t = s[0];
+      for (int i = 1; i < warps; ++i) {
+        const float4 u = s[i];
+        t.x += u.x;
+        if (N > 1) t.y += u.y;
+        if (N > 2) t.z += u.z;
+        if (N > 3) t.w += u.w;
+      }
+      v[0] = t.x;
+      if (N > 1) v[1 % N] = t.y;
+      if (N > 2) v[2 % N] = t.z;
+      if (N > 3) v[3 % N] = t.w;
+    } else {  // up to 16 warps: one value a lane, and exchanges
+      const int lane = threadIdx.x & 15;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lane < warps) t = s[lane];
+      v[0] = t.x;
+      if (N > 1) v[1 % N] = t.y;
+      if (N > 2) v[2 % N] = t.z;
+      if (N > 3) v[3 % N] = t.w;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    v[0] = t.x;
-    if (N > 1) v[1 % N] = t.y;
-    if (N > 2) v[2 % N] = t.z;
-    if (N > 3) v[3 % N] = t.w;
   }
 };
 
@@ -599,34 +614,47 @@ __global__ void __launch_bounds__(512)
   const int64_t rows = a.tokens * a.heads, pairs = (rows + R - 1) / R;
   unsigned char* mine = s_mem + threadIdx.x * 16;
   const unsigned dst0 = (unsigned)__cvta_generic_to_shared(mine);
-  auto fetch = [&](int slot, int64_t pair) {
+  // where the next pair to fetch lies; one step is the grid's pairs
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t next = (int64_t)blockIdx.x * R, next_at = next * a.width + col;
+  const int64_t step_at = step * a.width;
+  const IO* next_x = static_cast<const IO*>(a.x) + next * a.x_stride + col;
+  const IO* next_g = static_cast<const IO*>(a.gate) + next * a.gate_stride + col;
+  const int64_t step_x = step * a.x_stride, step_g = step * a.gate_stride;
+  auto fetch = [&](int slot) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      const int64_t row = pair * R + j;
-      if (row < rows) {
+      if (next + j < rows) {
         const unsigned dst = dst0 + slot * slot_bytes + j * row_units * unit;
-        const int64_t at = row * a.width + col;
-        send_vec<IO, VEC>(dst, unit, static_cast<const IO*>(a.x) + strided(a, row, a.x_stride) + col);
-        if (GATE)
-          send_vec<IO, VEC>(dst + UX * unit, unit,
-                            static_cast<const IO*>(a.gate) + strided(a, row, a.gate_stride) + col);
+        const int64_t at = next_at + j * a.width;
+        const IO *px = next_x + j * a.x_stride, *pg = next_g + j * a.gate_stride;
+        if (a.heads != 1) {
+          px = static_cast<const IO*>(a.x) + strided(a, next + j, a.x_stride) + col;
+          pg = static_cast<const IO*>(a.gate) + strided(a, next + j, a.gate_stride) + col;
+        }
+        send_vec<IO, VEC>(dst, unit, px);
+        if (GATE) send_vec<IO, VEC>(dst + UX * unit, unit, pg);
         if (pre) send_vec<IO, VEC>(dst + at_n * unit, unit, static_cast<const IO*>(a.d_normed) + at);
         if (res) send_vec<RT, VEC>(dst + at_r * unit, unit, static_cast<const RT*>(a.residual) + at);
         if (dout) send_vec<RT, VEC>(dst + at_o * unit, unit, static_cast<const RT*>(a.d_out) + at);
       }
     }
     asm volatile("cp.async.commit_group;");
+    next += step;
+    next_at += step_at;
+    next_x += step_x;
+    next_g += step_g;
   };
   f32x2 dpost[P], dscale[P], dpre[P];
 #pragma unroll
   for (int c = 0; c < P; ++c) dpost[c] = dscale[c] = dpre[c] = both(0.f);
   int slot = 0;
-  if (blockIdx.x < pairs) fetch(0, blockIdx.x);
+  if (blockIdx.x < pairs) fetch(0);
   __syncthreads();
   for (int64_t pair = blockIdx.x; pair < pairs; pair += gridDim.x, slot ^= 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     // the other slot's last reads lie behind the last pair's barriers
-    if (pair + gridDim.x < pairs) fetch(slot ^ 1, pair + gridDim.x);
+    if (pair + gridDim.x < pairs) fetch(slot ^ 1);
     const int64_t at = pair * R * a.width + col;
     const unsigned char* from = mine + slot * slot_bytes;
     bool on[R];
@@ -928,7 +956,7 @@ cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* p
   return cudaGetLastError();
 }
 
-constexpr int kFwd8[] = {4, 1}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8};
+constexpr int kFwd8[] = {2, 1, 4}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8};
 // rows that are not aligned: 16 elements a thread as far as 512 threads go
 constexpr int kOdd8[] = {2, 4}, kOdd4[] = {4, 8};
 
@@ -951,7 +979,7 @@ int unit_of(const NormArgs& a) {
 Shape shape_of(const NormArgs& a, bool bwd, int unit) {
   if (a.bf16)
     return unit < 8 ? row_shape(a, 8, kOdd8, 2)
-                    : bwd ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 8, kFwd8, 2);
+                    : bwd ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 8, kFwd8, 3);
   return unit < 4 ? row_shape(a, 4, kOdd4, 2)
                   : bwd ? row_shape(a, 4, kBwd4, 4) : row_shape(a, 4, kFwd4, 3);
 }
@@ -961,7 +989,7 @@ cudaError_t fwd_pick(const NormArgs& a, cudaStream_t st) {
   const Shape s = shape_of(a, false, UNIT);
   if constexpr (UNIT == VEC)
     if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1, UNIT>(a, s, st);
-  if constexpr (UNIT < VEC && VEC == 8)
+  if constexpr (VEC == 8)
     if (s.iter == 2) return fwd_launch<IO, RT, VEC, 2, UNIT>(a, s, st);
   if (s.iter == 4) return fwd_launch<IO, RT, VEC, 4, UNIT>(a, s, st);
   if constexpr (VEC == 4)
