@@ -280,10 +280,17 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     // place of every eighth or fourth exponential frees the special function
     // unit but is slower (0.51, 0.53 ms): issue slots bound the SM as well.
     f32x2 e01[2][4], e23[2][4], x01[2][4], x23[2][4];
+    // For the backward (and the ends of segments) a chunk's decay is put right
+    // at its end: the rounding of 8 exponentials, which would add up over a
+    // state's memory, gives way to that of one of the 8 steps' sum.
+    constexpr bool EXACT = MODE != kSsmOut;
+    f32x2 c01, c23, p01, p23;  // the chunk's start state, its product of decays
+    float sum4[2], chunk_sum = 0.f;
 #pragma unroll
     for (int q = 0; q <= kTile; q += 4) {
       const int next = q / 4 & 1, cur = next ^ 1;
       if (q < kTile) {
+        sum4[next] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // behind the last token: step 0 keeps the state
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           e23[next][j] = pack2(ex2_f(p[2]), ex2_f(p[3]));
           x01[next][j] = mul2(dtu, b.x);
           x23[next][j] = mul2(dtu, b.y);
-          if (MODE == kSsmEnds) steps += v.x;
+          if (EXACT) sum4[next] += v.x;
         }
       }
       if (q > 0) {
@@ -318,16 +325,35 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
               if (on && n0 + k < a.S) st[k] = v[k];
           }
         }
+        if (EXACT && t4 % kSsmChunk == 0) {
+          c01 = h01;
+          c23 = h23;
+          p01 = p23 = both(1.f);
+          chunk_sum = 0.f;
+        }
         float y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           h01 = fma2(e01[cur][j], h01, x01[cur][j]);
           h23 = fma2(e23[cur][j], h23, x23[cur][j]);
+          if (EXACT) {
+            p01 = mul2(p01, e01[cur][j]);
+            p23 = mul2(p23, e23[cur][j]);
+          }
           if (WANT_Y) {
             const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[w][t4 + j][n0]);
             float lo, hi;
             unpack2(fma2(h01, c.x, mul2(h23, c.y)), lo, hi);
             y[j] = lo + hi;
+          }
+        }
+        if (EXACT) {
+          chunk_sum += sum4[cur];
+          if (t4 % kSsmChunk == kSsmChunk - 4) {
+            chunk_decay(chunk_sum, A01, A23, p01, p23);
+            h01 = fma2(p01, c01, h01);
+            h23 = fma2(p23, c23, h23);
+            if (MODE == kSsmEnds) steps += chunk_sum;
           }
         }
         if (WANT_Y) {

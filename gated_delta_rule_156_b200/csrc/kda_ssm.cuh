@@ -99,6 +99,17 @@ struct SsmBlock {
   }
 };
 
+// p: a chunk's product of decays, as multiplied up; becomes what its decay
+// exp(sum of steps * A) has more than that.
+__device__ __forceinline__ void chunk_decay(float sum, f32x2 A01, f32x2 A23, f32x2& p01,
+                                            f32x2& p23) {
+  float x[4];
+  unpack2(mul2(both(sum), A01), x[0], x[1]);
+  unpack2(mul2(both(sum), A23), x[2], x[3]);
+  p01 = fma2(p01, both(-1.f), pack2(ex2_f(x[0]), ex2_f(x[1])));
+  p23 = fma2(p23, both(-1.f), pack2(ex2_f(x[2]), ex2_f(x[3])));
+}
+
 // Sum of NV values over the lanes that differ in the bits of `mask`, spread:
 // while there are values to halve, each exchange keeps one half of them; the
 // rest are plain exchanges.  Returns with v[0 .. NV/lanes) (at least one)

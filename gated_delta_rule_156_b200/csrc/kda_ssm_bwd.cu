@@ -379,6 +379,10 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     if (PARTS == 1) __syncthreads();
     for (int c = (m - 1) / K; c >= 0; --c) {
       const int tc = c * K;
+      // the chunk's decay is put right at its end, as in the forward kernel
+      const f32x2 g01 = dh01, g23 = dh23;
+      f32x2 p01 = both(1.f), p23 = both(1.f);
+      float sum = 0.f;
       if constexpr (ENDS) {
 #pragma unroll
         for (int t = K - 1; t >= 0; --t) {
@@ -388,10 +392,17 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           float p[4];
           unpack2(mul2(both(dt), A01), p[0], p[1]);
           unpack2(mul2(both(dt), A23), p[2], p[3]);
-          dh01 = mul2(fma2(dy, cv.x, dh01), pack2(ex2_f(p[0]), ex2_f(p[1])));
-          dh23 = mul2(fma2(dy, cv.y, dh23), pack2(ex2_f(p[2]), ex2_f(p[3])));
-          steps += dt;
+          const f32x2 e01 = pack2(ex2_f(p[0]), ex2_f(p[1])), e23 = pack2(ex2_f(p[2]), ex2_f(p[3]));
+          dh01 = mul2(fma2(dy, cv.x, dh01), e01);
+          dh23 = mul2(fma2(dy, cv.y, dh23), e23);
+          p01 = mul2(p01, e01);
+          p23 = mul2(p23, e23);
+          sum += dt;
         }
+        steps += sum;
+        chunk_decay(sum, A01, A23, p01, p23);
+        dh01 = fma2(p01, g01, dh01);
+        dh23 = fma2(p23, g23, dh23);
         continue;
       }
       f32x2 h01[K + 1], h23[K + 1], e01[K], e23[K];
@@ -423,6 +434,9 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         e23[t] = pack2(ex2_f(p[2]), ex2_f(p[3]));
         h01[t + 1] = fma2(e01[t], h01[t], mul2(dtu, bv.x));
         h23[t + 1] = fma2(e23[t], h23[t], mul2(dtu, bv.y));
+        p01 = mul2(p01, e01[t]);
+        p23 = mul2(p23, e23[t]);
+        sum += v.x;
       }
       f32x2 s01 = both(0.f), s23 = both(0.f);  // dA of the chunk
       float fed[4], qa[4];
@@ -469,6 +483,9 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       }
       dA01 = add2(dA01, s01);
       dA23 = add2(dA23, s23);
+      chunk_decay(sum, A01, A23, p01, p23);
+      dh01 = fma2(p01, g01, dh01);
+      dh23 = fma2(p23, g23, dh23);
     }
     __syncthreads();
   }
