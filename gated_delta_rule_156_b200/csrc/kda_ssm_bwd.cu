@@ -11,7 +11,9 @@
 // the sums above.  Sums over a channel's states are exchanges between its
 // lanes, sums over channels (dB, dC) exchanges between the warp's channels,
 // then shared memory, then one part per channel block in the workspace, which
-// a last kernel adds up: every order is fixed.
+// a last kernel adds up: every order is fixed.  Measured: 1.33 ms for 2 x 4096
+// tokens of 4096 channels with 16 states (0.35 the saving pass, 0.9 the pass
+// back), against 0.07 ms for the bytes alone.
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -53,8 +55,8 @@ struct BwdShared {
 // their decays in registers, and then back.  dB and dC are summed over the
 // warp's channels by exchanges: 8 values a token in 7 of them.  (Products with
 // a row of ones on the tensor cores, mma.sync in tf32, take fewer instructions
-// but were slower, 1.39 against 1.23 ms for 2 x 4096 tokens of 4096 channels,
-// and less exact.)  The kernel is bound by the issue of these instructions.
+// but were slower, 1.39 against 1.23 ms for 2 x 4096 tokens of 4096 channels
+// at the time, and less exact.)  The kernel is bound by the issue of these instructions.
 //
 // ENDS: a split scan's first pass backward (see SsmSplit): each segment's
 // gradient into its start state from none at its end, and its sum of steps.
