@@ -504,8 +504,8 @@ dim3 block_shape(int nvec) {
 }
 
 template <typename K>
-cudaError_t allow_shared(K kernel, int bytes) {
-  if (bytes <= 24 * 1024) return cudaSuccess;  // static shared memory comes on top
+cudaError_t allow_shared(K kernel, int bytes, int fixed) {  // fixed: static
+  if (bytes + fixed <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
@@ -529,7 +529,7 @@ cudaError_t fwd_launch(const ConvArgs& a, cudaStream_t stream) {
   const dim3 grid((unsigned)((rows + block.y - 1) / block.y), (nvec + block.x - 1) / block.x);
   constexpr int bytes = Ring<IO, VEC>::ON ? kStages * kGroup * 256 * Ring<IO, VEC>::BYTES : 0;
   auto* k = conv_fwd_kernel<IO, W, VEC>;
-  const cudaError_t e = allow_shared(k, bytes);
+  const cudaError_t e = allow_shared(k, bytes, 0);
   if (e != cudaSuccess) return e;
   if (rows) k<<<grid, block, bytes, stream>>>(a, nvec, run, n_runs);
   return cudaGetLastError();
@@ -573,7 +573,7 @@ cudaError_t bwd_launch(const ConvArgs& a, float* part, cudaStream_t stream) {
                   (nvec + kBwdLanes - 1) / kBwdLanes);
   constexpr int bytes = Ring<IO, VEC>::ON ? kStages * 2 * kGroup * 256 * Ring<IO, VEC>::BYTES : 0;
   auto* k = conv_bwd_kernel<IO, W, VEC>;
-  cudaError_t e = allow_shared(k, bytes);
+  cudaError_t e = allow_shared(k, bytes, kBwdRuns * (W + 1) * kBwdLanes * VEC * 4);
   if (e != cudaSuccess) return e;
   if (grid.x) k<<<grid, block, bytes, stream>>>(a, nvec, bwd_run(a), blocks, part);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -960,8 +960,9 @@ cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* p
 }
 
 constexpr int kFwd8[] = {2, 1, 4}, kFwd4[] = {4, 1, 8}, kBwd8[] = {2, 1, 4}, kBwd4[] = {2, 1, 4, 8};
-// rows that are not aligned: 16 elements a thread as far as 512 threads go
-constexpr int kOdd8[] = {2, 4}, kOdd4[] = {4, 8};
+// rows that are not aligned: 16 elements a thread as far as 512 threads go,
+// forward also one vector a thread for few rows
+constexpr int kOddFwd8[] = {2, 1, 4}, kOddFwd4[] = {4, 1, 8}, kOdd8[] = {2, 4}, kOdd4[] = {4, 8};
 
 // Neighbouring elements an access can take: 16 bytes of io where every
 // pointer, stride and the width allow it, 2 elements where they allow that.
@@ -981,17 +982,16 @@ int unit_of(const NormArgs& a) {
 
 Shape shape_of(const NormArgs& a, bool bwd, int unit) {
   if (a.bf16)
-    return unit < 8 ? row_shape(a, 8, kOdd8, 2)
+    return unit < 8 ? bwd ? row_shape(a, 8, kOdd8, 2) : row_shape(a, 8, kOddFwd8, 3)
                     : bwd ? row_shape(a, 8, kBwd8, 3) : row_shape(a, 8, kFwd8, 3);
-  return unit < 4 ? row_shape(a, 4, kOdd4, 2)
+  return unit < 4 ? bwd ? row_shape(a, 4, kOdd4, 2) : row_shape(a, 4, kOddFwd4, 3)
                   : bwd ? row_shape(a, 4, kBwd4, 4) : row_shape(a, 4, kFwd4, 3);
 }
 
 template <typename IO, typename RT, int VEC, int UNIT>
 cudaError_t fwd_pick(const NormArgs& a, cudaStream_t st) {
   const Shape s = shape_of(a, false, UNIT);
-  if constexpr (UNIT == VEC)
-    if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1, UNIT>(a, s, st);
+  if (s.iter == 1) return fwd_launch<IO, RT, VEC, 1, UNIT>(a, s, st);
   if constexpr (VEC == 8)
     if (s.iter == 2) return fwd_launch<IO, RT, VEC, 2, UNIT>(a, s, st);
   if (s.iter == 4) return fwd_launch<IO, RT, VEC, 4, UNIT>(a, s, st);

@@ -291,3 +291,57 @@ def test_tensors_of_another_device():
     assert torch.equal(a[0].cpu(), b[0].cpu())
     with pytest.raises(ValueError):
         K.short_conv_fwd(p["x"], q["w"])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_split_workspace_is_written_before_it_is_read(packed, monkeypatch):
+    # few channels: the scan and its backward run in segments
+    lens = [1500, 0, 3, 1200, 257]
+    T = sum(lens)
+    cu = torch.tensor(R.offsets_of(0, 0, lens), dtype=torch.int32,
+                      device=DEV) if packed else None
+    p = scan_layer(1, T, dtype=torch.bfloat16)
+
+    def calls():
+        kw = dict(D=p["D"], z=p["z"], cu_seqlens=cu)
+        args = (p["x"], p["delta"], p["A"], p["Bm"], p["Cm"])
+        a = K.ssm_scan_fwd(*args, **kw)
+        b = K.ssm_scan_bwd(*args, d_out=p["d_out"], **kw)
+        torch.cuda.synchronize()
+        return [t.clone() for t in (*a, *b) if t is not None]
+    kern, _ = K.ssm_scan_bwd_plan(1, T, 64, 16, 1, torch.bfloat16, packed,
+                                  len(lens))
+    assert kern == 6  # split
+    monkeypatch.delenv("KDA_WORKSPACE_FILL", raising=False)
+    want = calls()
+    monkeypatch.setenv("KDA_WORKSPACE_FILL", "127")
+    got = calls()
+    for i, (a, b) in enumerate(zip(want, got)):
+        assert torch.isfinite(b.float()).all(), i
+        assert torch.equal(a, b), i
+
+
+def test_graphs_replayed_on_two_streams():
+    # two captured backward passes replayed at once: each has its workspace
+    ps = [scan_layer(1, 1000, D=96, dtype=torch.bfloat16) for _ in range(2)]
+    ps[1]["delta"] = ps[1]["delta"] * 0.5
+
+    def run(p):
+        u, o, *_ = scan_forward(p)
+        return list(scan_backward(p, u, o).values())
+    want = [[t.clone() for t in run(p)] for p in ps]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for p in ps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(p))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in ps]
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(a, b) for a, b in zip(w, o))
