@@ -309,13 +309,13 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     }
     // sums over the helpers of one channel, in the order of the helpers
     float* s_sum = &sh.dt[0][0][0].x;  // [2][kHelpers][EC]
-    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers));
+    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
 #pragma unroll
     for (int j = 0; j < EC; ++j) {
       s_sum[hid * EC + j] = dskip[j];
       s_sum[(kHelpers + hid) * EC + j] = dbias[j];
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers));
+    asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
     for (int c = hid; c < blk.n; c += kHelpers) {
       float x = 0.f, y = 0.f;
       const int first = VEC ? c / E : c, step = VEC ? TPT : CH, j = VEC ? c % E : 0;
