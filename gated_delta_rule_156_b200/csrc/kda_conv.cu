@@ -19,7 +19,8 @@ namespace {
 
 // Tokens on their way: a ring of kStages groups of kGroup tokens in shared
 // memory, filled by asynchronous copies.  A thread copies just what it will
-// read itself (no barrier), and three groups in flight cost it no registers
+// read itself (no barrier; the copies are statements that the compiler moves no
+// read across), and three groups in flight cost it no registers
 // (2 x 8192 x 4096 forward: 55 us, 63 with the next group in registers).
 // Vectors of 4 elements; single elements are loaded 8 tokens at a time.
 constexpr int kGroup = 4, kStages = 4;
@@ -38,11 +39,13 @@ struct Ring {
   __device__ __forceinline__ static void send(unsigned char* to, const IO* from) {
     const unsigned dst = (unsigned)__cvta_generic_to_shared(to);
     if constexpr (BYTES == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(from));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(from) : "memory");
   }
-  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;"); }
+  __device__ __forceinline__ static void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   __device__ __forceinline__ static void wait() {  // for the oldest group in flight
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
   }

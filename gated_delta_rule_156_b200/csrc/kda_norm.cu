@@ -569,7 +569,8 @@ __device__ __forceinline__ void send_vec(unsigned dst, int unit, const T* p) {
 #pragma unroll
   for (int k = 0; k < kUnits<T, VEC>; ++k)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * unit),
-                 "l"(reinterpret_cast<const uint4*>(p) + k));
+                 "l"(reinterpret_cast<const uint4*>(p) + k)
+                 : "memory");
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void take_vec(const unsigned char* s, int unit, bool on,
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(512)
         if (dout) send_vec<RT, VEC>(dst + at_o * unit, unit, static_cast<const RT*>(a.d_out) + at);
       }
     }
-    asm volatile("cp.async.commit_group;");
+    asm volatile("cp.async.commit_group;" ::: "memory");
     next += step;
     next_at += step_at;
     next_x += step_x;

@@ -367,17 +367,18 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
                          (ssm_piece_id(seq, seq_start, K, (start - seq_start + t0) / K + c) * a.D + d) *
                              a.S + n0;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::
-                     "r"((unsigned)__cvta_generic_to_shared(&sh.state[w][c][tid])), "l"(p));
+                     "r"((unsigned)__cvta_generic_to_shared(&sh.state[w][c][tid])), "l"(p)
+                     : "memory");
       }
   };
   if (tiles > 0) fetch(tiles - 1, 0);
-  asm volatile("cp.async.commit_group;");
+  asm volatile("cp.async.commit_group;" ::: "memory");
   __syncthreads();
   for (int n = 0; n < tiles; ++n) {
     const int i = tiles - 1 - n, w = n & 1, m = min(kTile, end - start - i * kTile);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (i > 0) fetch(i - 1, w ^ 1);
-    asm volatile("cp.async.commit_group;");
+    asm volatile("cp.async.commit_group;" ::: "memory");
     if (PARTS == 1) __syncthreads();
     for (int c = (m - 1) / K; c >= 0; --c) {
       const int tc = c * K;

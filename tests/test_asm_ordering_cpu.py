@@ -1,8 +1,9 @@
 """Inline assembly that orders memory is ordered for the compiler as well.
 
-A barrier without a "memory" clobber holds the threads but not the compiler,
-which may move ordinary shared-memory accesses across it; whether it does is
-not visible in results, so the sources themselves are checked."""
+A barrier or an asynchronous copy without a "memory" clobber holds the threads
+but not the compiler, which may move ordinary shared-memory accesses across it;
+whether it does is not visible in results, so the sources themselves are
+checked."""
 import glob
 import os
 import re
@@ -49,3 +50,8 @@ def test_the_parser_finds_statements():
 
 def test_barriers_clobber_memory():
     assert without_clobber(r"\bbar\.sync|\bbarrier\.|\bmbarrier\.|\bfence\.") == []
+
+
+def test_asynchronous_copies_clobber_memory():
+    # a copy into a buffer must stay behind the last reads of what it held
+    assert without_clobber(r"\bcp\.async") == []
