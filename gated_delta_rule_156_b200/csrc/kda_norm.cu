@@ -888,6 +888,16 @@ cudaError_t fwd_launch(const NormArgs& a, const Shape& s, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Lets a kernel take shared memory beyond 48 KB.  The limit belongs to the
+// kernel on its device, not to a call, so every call sets the same one: with
+// its own size, a call of another host thread could lower it again before this
+// one's launch.
+constexpr int kMostShared = 226 * 1024;  // of the 227 KB a block may have; the sums take half a KB
+template <typename K>
+cudaError_t allow_shared(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+}
+
 // Shared memory of the backward for wide rows; 0 where it does not take them:
 // rows of 64 to 512 whole vectors in whole warps, a gate with a sigmoid, and
 // two slots that fit beside the weights.
@@ -903,7 +913,7 @@ PairShape pair_shape(const NormArgs& a, int vec) {
   const int row = a.width * (e * (1 + (a.gate ? 1 : 0) + (pre ? 1 : 0)) +
                              r * ((pre && a.residual ? 1 : 0) + (a.d_out ? 1 : 0)));
   const PairShape s{threads, kPairRows * row, 2 * kPairRows * row + 12 * a.width};
-  return s.bytes <= 226 * 1024 ? s : PairShape{0, 0, 0};
+  return s.bytes <= kMostShared ? s : PairShape{0, 0, 0};
 }
 
 // The most blocks of a backward launch: what its workspace holds parts for.
@@ -922,8 +932,7 @@ cudaError_t bwd_launch(const NormArgs& a, const Shape& s, int sms, float* part,
   const int per = s.block / s.tpr;
   const int bytes = per * 3 * ((a.width + 3) & ~3) * (int)sizeof(float);
   cudaError_t e = cudaSuccess;
-  if (bytes > 47 * 1024)  // the static part comes on top
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (bytes > 47 * 1024) e = allow_shared(k);  // the static part comes on top
   if (e != cudaSuccess) return e;
   int64_t blocks = resident_blocks(k, s.block, sms, bytes);
   const int64_t most = bwd_blocks(a, s, sms);
@@ -945,7 +954,7 @@ cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* p
                                    : norm_bwd_pair_kernel<IO, RT, VEC, 2, false>)
                            : (silu ? norm_bwd_pair_kernel<IO, RT, VEC, 1, true>
                                    : norm_bwd_pair_kernel<IO, RT, VEC, 1, false>);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, s.bytes);
+  cudaError_t e = allow_shared(k);
   if (e != cudaSuccess) return e;
   const int64_t need = (a.tokens * a.heads + kPairRows - 1) / kPairRows;
   int64_t blocks = resident_blocks(k, s.threads, sms, s.bytes);

@@ -1,4 +1,7 @@
 """kda_block_norm_fwd / _bwd against the 64-bit reference."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -226,3 +229,50 @@ def test_refusals():
     for f in bad:
         with pytest.raises((ValueError, K.KdaError)):
             f()
+
+
+@pytest.mark.parametrize("widths,act", [((4096, 2048), "sigmoid"),
+                                        ((8192, 6000), "none")])
+def test_threads_with_different_widths(widths, act):
+    # host threads in the same kernel with different amounts of shared memory:
+    # what one call allows the kernel must not be taken back by another before
+    # its launch.  The C calls alone, on prepared arguments, so that the
+    # threads are inside them (and without the interpreter's lock) most of the
+    # time
+    lib, calls, outs, want = K.library(), [], [], []
+    for w in widths:
+        d = make((64, w), "bf16", "bf16", w)
+        ins = [d[n] for n in NAMES] + [d["d_out"], d["d_normed"]]
+        kw = dict({n: d[n] for n in NAMES[1:]}, gate_act=act)
+        want.append(K.block_norm_bwd(d["x"], d_out=d["d_out"],
+                                     d_normed=d["d_normed"], **kw))
+        shape, _ = K._norm_shape(*ins[:6], torch.bfloat16, act, False, 1e-6)
+        for _ in range(2):  # two threads of each width
+            got = [torch.empty_like(t) for t in want[-1]]
+            outs.append((got, want[-1]))
+            calls.append((ctypes.byref(shape),
+                          *[t.data_ptr() for t in ins + got],
+                          torch.cuda.Stream(), ins))
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(calls))
+
+    def work(*args, stream, keep):
+        start.wait()
+        for _ in range(5000):
+            st = lib.kda_block_norm_bwd(*args, stream.cuda_stream)
+            if st != K.KDA_OK:
+                failed.append(st)
+                return
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=c[:-2],
+                                kwargs=dict(stream=c[-2], keep=c[-1]))
+               for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, [K.STATUS_NAMES[s] for s in failed]
+    torch.cuda.synchronize()
+    for got, ref in outs:
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
