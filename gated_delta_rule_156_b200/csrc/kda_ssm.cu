@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
 #pragma unroll
       for (int i = 0; i < kSsmStates; ++i)
         if (n0 + i < a.S)
-          h[i] = fmaf(ex2_f(sum * A2[i]), h[i], split.ends[row * a.S + n0 + i]);
+          h[i] = segment_join(ex2_f(sum * A2[i]), h[i], split.ends[row * a.S + n0 + i]);
     }
     if (!on)
 #pragma unroll
@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
           chunk_sum += sum4[cur];
           if (t4 % kSsmChunk == kSsmChunk - 4) {
             chunk_decay(chunk_sum, A01, A23, p01, p23);
-            h01 = fma2(p01, c01, h01);
-            h23 = fma2(p23, c23, h23);
+            chunk_add(p01, c01, h01);
+            chunk_add(p23, c23, h23);
             if (MODE == kSsmEnds) steps += chunk_sum;
           }
         }

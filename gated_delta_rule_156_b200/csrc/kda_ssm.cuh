@@ -16,6 +16,7 @@
 
 namespace kda {
 
+constexpr float kMaxFinite = 3.402823466e38f;
 constexpr int kSsmThreads = 128;
 constexpr int kSsmStates = 4;  // states per lane
 constexpr int kHelpers = 128;  // threads that feed the recurrence's 128
@@ -108,6 +109,21 @@ __device__ __forceinline__ void chunk_decay(float sum, f32x2 A01, f32x2 A23, f32
   unpack2(mul2(both(sum), A23), x[2], x[3]);
   p01 = fma2(p01, both(-1.f), pack2(ex2_f(x[0]), ex2_f(x[1])));
   p23 = fma2(p23, both(-1.f), pack2(ex2_f(x[2]), ex2_f(x[3])));
+}
+// Adds what the chunk's decay has more, p, times the chunk's start state c.
+// Where that is not finite nothing is added: with an infinite c the state is
+// what the single decays made of it, and a p that is not finite (a growth
+// beyond fp32) says nothing about a c of 0.
+__device__ __forceinline__ void chunk_add(f32x2 p, f32x2 c, f32x2& h) {
+  float lo, hi;
+  unpack2(mul2(p, c), lo, hi);
+  h = add2(h, pack2(fabsf(lo) <= kMaxFinite ? lo : 0.f, fabsf(hi) <= kMaxFinite ? hi : 0.f));
+}
+// A segment's end state from its start state h: decay * h + end, where an
+// infinite h stays infinite and a h of 0 stays 0, though the decay of all the
+// segment's tokens may be below or beyond what fp32 holds.
+__device__ __forceinline__ float segment_join(float decay, float h, float end) {
+  return isnan(decay * h) ? h + end : fmaf(decay, h, end);
 }
 
 // Sum of NV values over the lanes that differ in the bits of `mask`, spread:

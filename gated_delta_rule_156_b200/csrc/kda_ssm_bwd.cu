@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
 #pragma unroll
       for (int i = 0; i < kSsmStates; ++i)
         if (on && n0 + i < a.S)
-          g0[i] = fmaf(ex2_f(sum * A2[i]), g0[i], split.ends[row * a.S + n0 + i]);
+          g0[i] = segment_join(ex2_f(sum * A2[i]), g0[i], split.ends[row * a.S + n0 + i]);
     }
   }
   const f32x2 A01 = pack2(A2[0], A2[1]), A23 = pack2(A2[2], A2[3]);
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
         }
         steps += sum;
         chunk_decay(sum, A01, A23, p01, p23);
-        dh01 = fma2(p01, g01, dh01);
-        dh23 = fma2(p23, g23, dh23);
+        chunk_add(p01, g01, dh01);
+        chunk_add(p23, g23, dh23);
         continue;
       }
       f32x2 h01[K + 1], h23[K + 1], e01[K], e23[K];
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       dA01 = add2(dA01, s01);
       dA23 = add2(dA23, s23);
       chunk_decay(sum, A01, A23, p01, p23);
-      dh01 = fma2(p01, g01, dh01);
-      dh23 = fma2(p23, g23, dh23);
+      chunk_add(p01, g01, dh01);
+      chunk_add(p23, g23, dh23);
     }
     __syncthreads();
   }

@@ -137,6 +137,8 @@ typedef struct {
  * the SMs idle are scanned in segments side by side, which are then joined
  * (exactly: the recurrence is linear in the state); that takes stream-ordered
  * workspace of D (S + 1) floats a segment.
+ * An infinite state stays infinite while its tokens' decays are above 0 in
+ * fp32, split or not (0 times infinity, behind such a decay, may be NaN).
  */
 KDA_API kda_status kda_ssm_scan_fwd(
     const kda_ssm_shape* shape, const void* u, const void* delta,

@@ -402,3 +402,54 @@ def test_split_backward_repeats_and_matches_one_segment():
             R.check("d " + name, x, y.cpu().double(), 4 * tol(T) + n * 2.0 ** -24)
         else:
             R.check("d " + name, x, y[:1].cpu().double(), 4 * tol(T))
+
+
+@pytest.mark.parametrize("copies", [1, 200])
+def test_infinite_states_stay_infinite(copies):
+    # one sequence in segments, and enough copies of it not to be split: a
+    # decay greater than 0 leaves an infinite state infinite, also where the
+    # decay of a whole segment is too small for fp32
+    T, D, S = 1500, 64, 16
+    d = make((1, T), D, S, 1, "f32", 41, past=1)
+    d["past"][0, 7, 3] = float("inf")
+    d["past"][0, 9, 0] = float("-inf")
+    d["past"][0, 9, 1] = float("nan")
+    d["A"][7, 3] = -3.0  # a segment's decay is around exp(-140)
+
+    def many(t):
+        return t.expand(copies, *t.shape[1:]).contiguous()
+    kw = dict(D=d["D"], delta_bias=d["delta_bias"],
+              initial_state=many(d["past"]))
+    args = (many(d["u"]), many(d["delta"]), d["A"], many(d["Bm"]),
+            many(d["Cm"]))
+    out, fin = K.ssm_scan_fwd(*args, **kw)
+    want = many(d["past"])
+    bad = ~torch.isfinite(want)
+    assert torch.equal(torch.isfinite(fin), ~bad)
+    assert torch.equal(fin[bad].nan_to_num(7.0), want[bad].nan_to_num(7.0))
+    assert torch.isinf(out[:, :, 7]).all() and torch.isnan(out[:, :, 9]).all()
+    ok = [c for c in range(D) if c not in (7, 9)]
+    assert torch.isfinite(out[:, :, ok]).all()
+    # backward: dC = dy h sees the infinite state (and, with it, NaN), the
+    # gradients that no state enters do not
+    got = K.ssm_scan_bwd(*args, d_out=many(d["d_out"]), **kw)
+    assert torch.isinf(got[4][..., 3]).all()
+    for i in (0, 3, 8):
+        assert torch.isfinite(got[i]).all(), NAMES[i]
+    assert torch.isfinite(got[4][..., 4:]).all()
+
+
+@pytest.mark.parametrize("copies", [1, 200])
+def test_growth_of_nothing_is_nothing(copies):
+    # a positive A: eight tokens' growth is beyond fp32, but a state of 0
+    # stays 0 until an input comes
+    T, D = 1000, 64
+    u = torch.zeros(copies, T, D, device=DEV)
+    delta = torch.zeros_like(u)
+    A = torch.full((D, 16), 50.0, device=DEV)
+    bc = torch.ones(copies, T, 1, 16, device=DEV)
+    out, fin = K.ssm_scan_fwd(u, delta, A, bc, bc)
+    assert (out == 0).all() and (fin == 0).all()
+    got = K.ssm_scan_bwd(u, delta, A, bc, bc, d_out=torch.zeros_like(u))
+    for x in got:
+        assert x is None or (x == 0).all()
