@@ -724,6 +724,14 @@ def _sequences(x, dev, cu_seqlens):
     return n, n
 
 
+def _dims(*sizes):
+    """The sizes of a call, refused where one does not fit the C ABI's 32-bit
+    fields (ctypes would cut it)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"every size must be below 2^31, got {sizes}")
+    return sizes
+
+
 def _empty(t):
     """An uninitialised dense tensor of t's shape and dtype."""
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
@@ -748,7 +756,7 @@ def _conv_shape(x, weight, bias, cu_seqlens, activation):
     W = weight.shape[1]
     _need("weight", weight, dev, f32, (D, W))
     _need("bias", bias, dev, f32, (D,), optional=True)
-    shape = KdaConvShape(B, T, D, W, packed, _io(x), ACTS[activation],
+    shape = KdaConvShape(*_dims(B, T, D, W, packed), _io(x), ACTS[activation],
                          _tokens("x", x, dev, x.dtype, full))
     return shape, dev, full, (n, W - 1, D)
 
@@ -832,8 +840,8 @@ def _ssm_shape(u, delta, A, Bm, Cm, D, z, delta_bias, cu_seqlens, softplus):
     zs = 0 if z is None else _tokens("z", z, dev, dt, full)
     bs, bg = _groups("Bm", Bm, dev, dt, (B, T, G, S))
     cs, cg = _groups("Cm", Cm, dev, dt, (B, T, G, S))
-    shape = KdaSsmShape(B, T, C, S, G, packed, _io(u), 1 if softplus else 0,
-                        us, ds, zs, bs, bg, cs, cg)
+    shape = KdaSsmShape(*_dims(B, T, C, S, G, packed), _io(u),
+                        1 if softplus else 0, us, ds, zs, bs, bg, cs, cg)
     return shape, dev, full, (n, C, S)
 
 
@@ -896,7 +904,7 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None,
 def ssm_scan_bwd_plan(B, T, D, S, G, dtype, packed=False, n_seqs=0):
     """(kernels, workspace_bytes) of an ssm_scan_bwd call of this shape."""
     io = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    shape = KdaSsmShape(B, T, D, S, G, n_seqs if packed else 0, io, 1)
+    shape = KdaSsmShape(*_dims(B, T, D, S, G, n_seqs if packed else 0), io, 1)
     kern, ws = ctypes.c_int(), ctypes.c_size_t()
     st = library().kda_ssm_scan_bwd_plan(ctypes.byref(shape), int(packed),
                                          ctypes.byref(kern), ctypes.byref(ws))
@@ -946,7 +954,7 @@ def _norm_shape(x, post_weight, gate, residual, scale, pre_weight, rt,
     gs = 0 if gate is None else _tokens("gate", gate, dev, dt, x.shape, inner)
     if rt not in (dt, f32):
         raise ValueError(f"the residual must be {dt} or float32, got {rt}")
-    return KdaNormShape(tokens, max(heads, 1), width, _io(x),
+    return KdaNormShape(tokens, *_dims(max(heads, 1), width), _io(x),
                         KDA_BF16 if rt == torch.bfloat16 else KDA_F32,
                         ACTS[gate_act], 1 if gate_first else 0, eps, xs,
                         gs), dev

@@ -7,6 +7,7 @@ import sys
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 import layer_ref as R
 from gated_delta_rule_156_b200 import build as kbuild
@@ -154,3 +155,31 @@ def test_saved_state_ids_never_meet():
                 seen.add(i)
             start += length
         assert not seen or max(seen) < start // 8 + n + 1
+
+
+def test_sizes_beyond_the_abi_fields_are_refused():
+    # 2^32 + 5 tokens must not reach the 32-bit field as 5; the tensors are
+    # fakes without memory
+    big, bf = 2 ** 32 + 5, torch.bfloat16
+    with FakeTensorMode():
+        def fake(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device="cuda")
+        x, w = fake(1, big, 1, dtype=bf), fake(1, 4)
+        bc = fake(1, big, 1, 1, dtype=bf)
+        calls = [
+            lambda: K._conv_shape(x, w, None, None, "silu"),
+            lambda: K._conv_shape(fake(1, 5, 1), w, None,
+                                  fake(big, dtype=torch.int32), "silu"),
+            lambda: K._ssm_shape(x, x, fake(1, 1), bc, bc, None, None, None,
+                                 None, True),
+            lambda: K._norm_shape(fake(3, big, dtype=bf), None, None, None,
+                                  None, None, bf, "none", False, 1e-6),
+            lambda: K.ssm_scan_bwd_plan(1, big, 64, 16, 1, bf),
+        ]
+        for call in calls:
+            with pytest.raises(ValueError, match="2\\^31"):
+                call()
+        # the number of the norm's rows has 64 bits
+        shape, _ = K._norm_shape(fake(big, 3, dtype=bf), None, None, None,
+                                 None, None, bf, "none", False, 1e-6)
+        assert shape.tokens == big and shape.width == 3
