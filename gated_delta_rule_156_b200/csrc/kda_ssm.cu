@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       for (int j = 0; j < E; ++j) {
         const float raw = r.d.get(j) + bias[VEC ? j : 0], uu = r.u.get(j);
         const bool real = tok_of(j) < m && ch_of(j) < blk.n;
-        dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
+        dt[j] = real ? (a.softplus ? softplus_f<IO>(raw) : raw) : 0.f;
         dtu[j] = dt[j] * uu;
         if (WANT_Y) {
           add_[j] = skip[VEC ? j : 0] * uu;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
       const float raw = to_f32(static_cast<const IO*>(a.delta)[tok * a.delta_stride + d]) + bias;
       const float uu = to_f32(static_cast<const IO*>(a.u)[tok * a.u_stride + d]);
       const float gz = a.z ? to_f32(static_cast<const IO*>(a.z)[tok * a.z_stride + d]) : 0.f;
-      const float dt0 = a.softplus ? softplus_f(raw) : raw, dtu0 = dt0 * uu;
+      const float dt0 = a.softplus ? softplus_f<IO>(raw) : raw, dtu0 = dt0 * uu;
       float y[NS];
 #pragma unroll
       for (int k = 0; k < NS; ++k) {

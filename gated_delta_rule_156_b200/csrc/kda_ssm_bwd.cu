@@ -20,8 +20,6 @@ namespace kda {
 
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-
 struct BwdParts {
   float* states;   // [piece ids of 8 tokens][D][S]
   float* bc;       // [channel block][token][2][S]
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
       for (int j = 0; j < E; ++j) {
         const float raw = rd.get(j) + bias[VEC ? j : 0];
         const bool real = tok_of(j) < m && ch_of(j) < blk.n;
-        dt[j] = real ? (a.softplus ? softplus_f(raw) : raw) : 0.f;
+        dt[j] = real ? (a.softplus ? softplus_f<IO>(raw) : raw) : 0.f;
         dtu[j] = ENDS ? 0.f : dt[j] * ru.get(j);
         dy[j] = ro.get(j);
         if (z) {

@@ -453,3 +453,23 @@ def test_growth_of_nothing_is_nothing(copies):
     got = K.ssm_scan_bwd(u, delta, A, bc, bc, d_out=torch.zeros_like(u))
     for x in got:
         assert x is None or (x == 0).all()
+
+
+def test_steps_keep_their_relative_accuracy():
+    # with u = B = 1 and no past a single token's state is its step, and with
+    # one channel d_B is the step as well.  Units of 2^-24: the exponential 4,
+    # its argument's remainder 1, 2 + e 1, the reciprocal 2, their product 1,
+    # the series 1, the last product 1
+    bound = 11 * 2.0 ** -24
+    delta = torch.linspace(-80, 20, 4001, device=DEV).reshape(-1, 1, 1)
+    want = torch.nn.functional.softplus(delta.double(), threshold=60)
+    one = torch.ones_like(delta)
+    A, bc = -torch.ones(1, 1, device=DEV), one.unsqueeze(-1)
+    _, fin = K.ssm_scan_fwd(one, delta, A, bc, bc)
+    state = torch.zeros_like(fin)
+    K.ssm_step(one, delta, A, bc, bc, state)
+    got = K.ssm_scan_bwd(one, delta, A, bc, bc, d_out=one)
+    for name, x in (("prompt", fin), ("token", state), ("backward", got[3])):
+        worst = (x.reshape(want.shape).double() / want - 1).abs().max()
+        assert worst <= bound, f"{name}: {float(worst):.3e} > {bound:.3e}"
+
