@@ -281,10 +281,15 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     // place of every eighth or fourth exponential frees the special function
     // unit but is slower (0.51, 0.53 ms): issue slots bound the SM as well.
     f32x2 e01[2][4], e23[2][4], x01[2][4], x23[2][4];
-    // For the backward (and the ends of segments) a chunk's decay is put right
-    // at its end: the rounding of 8 exponentials, which would add up over a
-    // state's memory, gives way to that of one of the 8 steps' sum.
-    constexpr bool EXACT = MODE != kSsmOut;
+    // A chunk's decay is put right at its end: the rounding of 8 exponentials,
+    // which would add up over a state's memory, gives way to that of one of the
+    // 8 steps' sum.  Without it in bf16 prompts alone: a bf16 step is itself off
+    // by 2^-9 of its value, so its decay by 2^-9 of its exponent, where 8
+    // exponentials' rounding is 2^-19 at most; the correction costs 8 % there
+    // (541 against 499 us, 2 x 8192 x 4096).  In fp32 it takes 3 % (214 -> 221
+    // us, 2 x 4096 x 2048) and the state's error from 1.3e-6 to 5e-7 (8 x 1024
+    // tokens, steps of 0.001 to 0.1).
+    constexpr bool EXACT = MODE != kSsmOut || sizeof(IO) == 4;
     f32x2 c01, c23, p01, p23;  // the chunk's start state, its product of decays
     float sum4[2], chunk_sum = 0.f;
 #pragma unroll

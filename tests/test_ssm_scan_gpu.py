@@ -473,3 +473,49 @@ def test_steps_keep_their_relative_accuracy():
         worst = (x.reshape(want.shape).double() / want - 1).abs().max()
         assert worst <= bound, f"{name}: {float(worst):.3e} > {bound:.3e}"
 
+
+
+@pytest.mark.parametrize("copies", [1, 200])
+def test_a_decay_is_as_good_as_its_chunks(copies):
+    # States of 1 that only decay, over T equal steps: a factor's error comes
+    # T times, so what counts is how many factors there are.  The error of one
+    # exponential is read off a single token: of one step (the factor of a
+    # token) and of eight (that of a chunk, the steps' sum being exact here).
+    # A scan that multiplies tokens' factors misses by T times the first; held
+    # to chunks it may miss by T / 8 times the second, plus the rounding of
+    # the running products (2 a token, independent, 4 standard deviations of
+    # 2^-24 at most) and of 16 segments' exponentials (2^-21 each).  The
+    # chunk's own product, which its exponential replaces, is 8 equal factors
+    # multiplied up from 1: 7 products, each off by up to 2^-25, and by the
+    # same in every chunk, so T / 8 times 7 2^-25 more.
+    T, D, S, dt = 2048, 64, 16, 2.0 ** -10
+    g = torch.Generator(device=DEV).manual_seed(17)
+    A = -(0.1 + 0.9 * torch.rand(D, S, generator=g, device=DEV))
+
+    def inputs(n, t, step):
+        u = torch.zeros(n, t, D, device=DEV)
+        bc = torch.ones(n, t, 1, S, device=DEV)
+        return u, torch.full_like(u, step), A, bc, bc
+
+    def one_factor(step):  # its relative error
+        state = torch.ones(1, D, S, device=DEV)
+        K.ssm_step(*inputs(1, 1, step), state, softplus=False)
+        return state.double() / torch.exp(step * A.double()) - 1
+
+    start = torch.ones(copies, D, S, device=DEV)
+    args = inputs(copies, T, dt)
+    _, fin = K.ssm_scan_fwd(*args, initial_state=start, softplus=False)
+    got = K.ssm_scan_bwd(*args, initial_state=start, softplus=False,
+                         d_out=torch.zeros_like(args[0]), d_final_state=start)
+    want = torch.exp(T * dt * A.double())
+    own = T / 8 * one_factor(8 * dt).abs()
+    bound = own + T / 8 * 7 * 2.0 ** -25 + \
+        4 * (2 * T) ** 0.5 * 2.0 ** -24 + 16 * 2.0 ** -21
+    # the bound means something: many a state's factors would break it
+    assert (T * one_factor(dt).abs() > bound).float().mean() > 0.05
+    for name, x in (("final state", fin), ("d_initial_state", got[8]),
+                    # T dt h dh, one term a token and copy, of two decays
+                    ("dA", got[2][None] / (copies * T * dt))):
+        err = (x.double() / want - 1).abs()
+        over = (err / (2 * bound if name == "dA" else bound)).max()
+        assert over <= 1, f"{name}: {float(over):.2f} of the bound"
