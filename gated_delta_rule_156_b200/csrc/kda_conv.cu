@@ -555,7 +555,8 @@ cudaError_t step_launch(const ConvArgs& a, cudaStream_t stream) {
 
 // Tokens a thread takes backward: 64 (which reads 3 of 67 again and sums 512
 // tokens before a part is written), fewer where that would not give every SM
-// its two blocks.
+// its two blocks (in fp32 one: the ring's 128 KB and the parts' 20 leave no room
+// for a second).
 int bwd_run(const ConvArgs& a) {
   int run = 64;
   while (run > 8 && a.tokens / run * (a.D / 4) < (int64_t)148 * 512) run /= 2;

@@ -133,7 +133,7 @@ __device__ __forceinline__ float silu_grad(float x, float s) {
 // argument p costs e up to 2^-25 |p|.  For an fp32 x what p lacks is put into
 // e; a bf16 x is itself rounded by 2^-9 of its value, which costs e 2^15 times
 // as much, and keeps the shorter form (a prompt of 2 x 8192 x 4096 in bf16 500
-// us, 517 with the longer one).
+// us, 517 with the longer one; 2 x 4096 x 2048 in fp32 207 and 214 us).
 template <typename IO>
 __device__ __forceinline__ float softplus_f(float x) {
   float e, top = fmaxf(x, 0.f);

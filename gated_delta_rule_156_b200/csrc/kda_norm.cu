@@ -7,8 +7,10 @@
 // Backward of y = rms(v) w:  dv = r (dy w - vhat mean(dy w vhat)),
 // dw = sum over rows of dy vhat, with vhat = v r.
 //
-// A row is read once and its elements stay in registers across both norms, so
-// HBM is the bound; to reach it, a row's fixed cost (its sums over threads, its
+// A row is read once and its elements stay in registers across both norms (up
+// to 8192 columns; wider rows hold 32 elements a thread, and all but the aligned
+// forward without a gate spill some of them: 4096 x 16384 forward 189 us, 55 % of
+// a copy's rate, backward 1104 us), so HBM is the bound; to reach it, a row's fixed cost (its sums over threads, its
 // addresses) must be spread over many elements a thread.  Work split: TPR
 // threads own a row (part of a warp for a head's row, a block for a wide one)
 // with 16 elements a thread (32 in the widest rows), and several blocks an SM,
@@ -20,7 +22,8 @@
 // the rows do not stay.  The grid is the resident blocks only.  Measured, in
 // shares of a copy's rate: 16384 x 4096 with an fp32 residual 178 us (82 %),
 // 524288 rows of 128 with a gate 85 us (73 %), backward of 8192 x 4096 143 us
-// (58 %, bound by issue).
+// (58 %; issue slots half used: three sums over the block a pair of rows, with
+// one block of 16 warps an SM and nothing to run under them).
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -5,8 +5,11 @@
 // Bound: an update costs one exponential and about 6 flops.  The special
 // function unit gives 16 a cycle and SM, so 16 states a channel cost more
 // there (0.24 ms for 2 x 8192 tokens of 4096 channels at 1.9 GHz) than the
-// 8 bytes a token and channel cost in HBM (0.08 ms).  Measured: 0.50 ms, with
-// the issue slots of the busy SMs as full as their special function units.
+// 8 bytes a token and channel cost in HBM (0.08 ms).  Measured: 0.50 ms (fp32,
+// see EXACT below: 0.58).  Neither is full then: an SM with two CTAs uses 71 %
+// of its special function unit and 61 % of its issue slots, 256 CTAs give 40 of
+// 148 SMs only one, and the rest is latency at 16 warps an SM.  More than 64
+// states in bf16 spill about 550 bytes a thread.
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -279,16 +282,18 @@ __global__ void __launch_bounds__(kSsmThreads + kHelpers, 2)
     // that exponentials and the rest alternate (a loop over 8 tokens: 0.54 ms
     // against 0.50 for 2 x 8192 tokens of 4096 channels).  A polynomial in
     // place of every eighth or fourth exponential frees the special function
-    // unit but is slower (0.51, 0.53 ms): issue slots bound the SM as well.
+    // unit but is slower (0.51, 0.53 ms): the instructions it takes cost more than
+    // the unit's share that it frees.
     f32x2 e01[2][4], e23[2][4], x01[2][4], x23[2][4];
     // A chunk's decay is put right at its end: the rounding of 8 exponentials,
     // which would add up over a state's memory, gives way to that of one of the
     // 8 steps' sum.  Without it in bf16 prompts alone: a bf16 step is itself off
     // by 2^-9 of its value, so its decay by 2^-9 of its exponent, where 8
     // exponentials' rounding is 2^-19 at most; the correction costs 8 % there
-    // (541 against 499 us, 2 x 8192 x 4096).  In fp32 it takes 3 % (214 -> 221
-    // us, 2 x 4096 x 2048) and the state's error from 1.3e-6 to 5e-7 (8 x 1024
-    // tokens, steps of 0.001 to 0.1).
+    // (541 against 499 us, 2 x 8192 x 4096).  In fp32 it takes the state's error
+    // from 1.3e-6 to 5e-7 (8 x 1024 tokens, steps of 0.001 to 0.1), below what
+    // correctly rounded exponentials leave (2.3e-6), and costs 10 % together with
+    // the longer softplus (525 -> 578 us, 2 x 8192 x 4096).
     constexpr bool EXACT = MODE != kSsmOut || sizeof(IO) == 4;
     f32x2 c01, c23, p01, p23;  // the chunk's start state, its product of decays
     float sum4[2], chunk_sum = 0.f;

@@ -22,7 +22,7 @@ constexpr int kSsmStates = 4;  // states per lane
 constexpr int kHelpers = 128;  // threads that feed the recurrence's 128
 
 // Tokens per tile: 32; 16 where two lanes a channel give the CTA 64 channels
-// (a helper then holds 8 pairs as with four lanes, and nothing spills).
+// (a helper then holds 8 pairs as with four lanes, 16 with a tile of 32).
 constexpr int tile_of(int lanes) { return lanes == 2 ? 16 : 32; }
 
 // N elements on their way from memory, as the 32-bit registers that the loads

@@ -11,9 +11,9 @@
 // the sums above.  Sums over a channel's states are exchanges between its
 // lanes, sums over channels (dB, dC) exchanges between the warp's channels,
 // then shared memory, then one part per channel block in the workspace, which
-// a last kernel adds up: every order is fixed.  Measured: 1.33 ms for 2 x 4096
+// a last kernel adds up: every order is fixed.  Measured: 1.29 ms for 2 x 4096
 // tokens of 4096 channels with 16 states (0.35 the saving pass, 0.9 the pass
-// back), against 0.07 ms for the bytes alone.
+// back), against 0.07 ms for the bytes alone; 1.34 ms in fp32.
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -54,7 +54,12 @@ struct BwdShared {
 // warp's channels by exchanges: 8 values a token in 7 of them.  (Products with
 // a row of ones on the tensor cores, mma.sync in tf32, take fewer instructions
 // but were slower, 1.39 against 1.23 ms for 2 x 4096 tokens of 4096 channels
-// at the time, and less exact.)  The kernel is bound by the issue of these instructions.
+// at the time, and less exact.)  No unit is full (issue slots 48 % used, shared
+// memory 45, FMA pipe 32, special function unit 20): what bounds the kernel is
+// latency at the 16 warps an SM that 128 registers leave, and the barrier a tile
+// that ties the recurrence to its helpers, the largest stall.  At those 128
+// registers every variant spills, 4 to 100 bytes a thread in bf16 and up to 232
+// in fp32.
 //
 // ENDS: a split scan's first pass backward (see SsmSplit): each segment's
 // gradient into its start state from none at its end, and its sum of steps.
