@@ -1369,12 +1369,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
-}
-
 // 16-byte loads each thread keeps in flight while staging a tensor-core
 // operand (the staging is bound by their latency; eight and four measured
 // slower than four and two).
@@ -1640,7 +1634,7 @@ cudaError_t launch_bmm_tc_t(const BmmOp& op, const BmmMaps& maps, int mask,
   for (int t = 0; t < op.nterms; ++t)
     kdmax = op.term[t].kd > kdmax ? op.term[t].kd : kdmax;
   const size_t smem = (size_t)(kdmax / 32) * (MD + ND) * 128 + 1024 + 64;
-  cudaError_t e = set_smem(bmm_tc_kernel<MD, ND>, smem);
+  cudaError_t e = allow_shared(bmm_tc_kernel<MD, ND>);
   if (e != cudaSuccess) return e;
   // items per CTA: 4, 2 or 1, whichever still leaves two resident waves
   const int64_t items = (int64_t)grid.x * grid.y;
@@ -1715,7 +1709,7 @@ cudaError_t launch_bmm_t(const BmmOp& op, size_t smem, dim3 grid,
                          cudaStream_t stream, const int32_t* cu,
                          const int32_t* co, int n_seqs, int T, int H, int dk,
                          int dv, int C) {
-  cudaError_t e = set_smem(bmm_kernel<RM, RN>, smem);
+  cudaError_t e = allow_shared(bmm_kernel<RM, RN>);
   if (e != cudaSuccess) return e;
   bmm_kernel<RM, RN><<<grid, kThreads, smem, stream>>>(op, cu, co, n_seqs, T, H,
                                                        dk, dv, C);
@@ -1781,18 +1775,18 @@ cudaError_t run_bwd(const BwdArgs& a, void* workspace, cudaStream_t stream) {
           reinterpret_cast<const __nv_bfloat16*>(a.d_out)};
       if (dk == 128) {
         const size_t sz = PrepTcLayout<128>::bytes + 1024;
-        if ((e = set_smem(prep_tc_kernel<128>, sz)) != cudaSuccess) return e;
+        if ((e = allow_shared(prep_tc_kernel<128>)) != cudaSuccess) return e;
         prep_tc_kernel<128><<<grid, kThreads, sz, stream>>>(
             b16[0], b16[1], b16[2], f.beta, b16[3], w.fv.g, w, cu, co,
             f.n_seqs, f.T, H, dv);
       } else {
         const size_t sz = PrepTcLayout<64>::bytes + 1024;
-        if ((e = set_smem(prep_tc_kernel<64>, sz)) != cudaSuccess) return e;
+        if ((e = allow_shared(prep_tc_kernel<64>)) != cudaSuccess) return e;
         prep_tc_kernel<64><<<grid, kThreads, sz, stream>>>(
             b16[0], b16[1], b16[2], f.beta, b16[3], w.fv.g, w, cu, co,
             f.n_seqs, f.T, H, dv);
       }
-    } else if ((e = set_smem(prep_kernel<IO>, smp)) != cudaSuccess) {
+    } else if ((e = allow_shared(prep_kernel<IO>)) != cudaSuccess) {
       return e;
     } else {
     prep_kernel<IO><<<grid, kThreads, smp, stream>>>(
@@ -1914,7 +1908,7 @@ cudaError_t run_bwd(const BwdArgs& a, void* workspace, cudaStream_t stream) {
     constexpr int tp = kChainTile + 1;
     const size_t smc = 4 * ((size_t)dk * tp + 2 * (size_t)C * (dk + 1) +
                             (size_t)C * tp + dk);
-    if ((e = set_smem(chain_kernel<kChainTile>, smc)) != cudaSuccess) return e;
+    if ((e = allow_shared(chain_kernel<kChainTile>)) != cudaSuccess) return e;
     chain_kernel<kChainTile><<<dim3(f.n_seqs, H, dv / kChainTile), kThreads,
                                smc, stream>>>(w, a.d_final_state,
                                               a.d_initial_state, cu, f.n_seqs,
@@ -1958,7 +1952,7 @@ cudaError_t run_bwd(const BwdArgs& a, void* workspace, cudaStream_t stream) {
                kMaskNone, 1.f, 0))
 #undef KDA_BMM
   const size_t smf = 4 * (size_t)C * dk + (size_t)C * dk;
-  if ((e = set_smem(final_kernel<IO>, smf)) != cudaSuccess) return e;
+  if ((e = allow_shared(final_kernel<IO>)) != cudaSuccess) return e;
   final_kernel<IO><<<grid, kThreads, smf, stream>>>(
       w, static_cast<const IO*>(f.q), static_cast<const IO*>(f.k),
       static_cast<const IO*>(f.v), f.beta,

@@ -23,6 +23,19 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// The most shared memory that a block can have.
+constexpr int kBlockShared = 227 * 1024;
+
+// Lets a kernel's launches take more than 48 KB of dynamic shared memory, up to
+// `most` (kBlockShared less the kernel's static shared memory).  The limit
+// belongs to the kernel on its device and not to a launch, so it has to be one
+// number for all launches of a kernel: set to each launch's own size, a call of
+// another host thread could lower it again before this one's launch.
+template <typename K>
+cudaError_t allow_shared(K kernel, int most = kBlockShared) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) {
   return x < lo ? lo : (x > hi ? hi : x);
 }

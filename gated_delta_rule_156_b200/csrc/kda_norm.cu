@@ -8,22 +8,23 @@
 // dw = sum over rows of dy vhat, with vhat = v r.
 //
 // A row is read once and its elements stay in registers across both norms (up
-// to 8192 columns; wider rows hold 32 elements a thread, and all but the aligned
-// forward without a gate spill some of them: 4096 x 16384 forward 189 us, 55 % of
-// a copy's rate, backward 1104 us), so HBM is the bound; to reach it, a row's fixed cost (its sums over threads, its
-// addresses) must be spread over many elements a thread.  Work split: TPR
-// threads own a row (part of a warp for a head's row, a block for a wide one)
-// with 16 elements a thread (32 in the widest rows), and several blocks an SM,
-// so that one row's loads run under another's sums.  (With 8 elements a
-// thread and one or two blocks an SM, rows prefetched through registers or an
-// asynchronous ring included, 16384 x 4096 took 0.21 to 0.33 ms.)  Each thread
-// meets the same elements of every row, so the weights' gradients are sums of
-// its own, kept in shared memory backward; the weights come out of L1, where
-// the rows do not stay.  The grid is the resident blocks only.  Measured, in
-// shares of a copy's rate: 16384 x 4096 with an fp32 residual 178 us (82 %),
-// 524288 rows of 128 with a gate 85 us (73 %), backward of 8192 x 4096 143 us
-// (58 %; issue slots half used: three sums over the block a pair of rows, with
-// one block of 16 warps an SM and nothing to run under them).
+// to 8192 columns; wider rows hold 32 elements a thread, and all but the
+// aligned forward without a gate spill some of them: 4096 x 16384 forward 189
+// us, 55 % of a copy's rate, backward 1104 us), so HBM is the bound; to reach
+// it, a row's fixed cost (its sums over threads, its addresses) must be spread
+// over many elements a thread.  Work split: TPR threads own a row (part of a
+// warp for a head's row, a block for a wide one) with 16 elements a thread (32
+// in the widest rows), and several blocks an SM, so that one row's loads run
+// under another's sums.  (With 8 elements a thread and one or two blocks an SM,
+// rows prefetched through registers or an asynchronous ring included, 16384 x
+// 4096 took 0.21 to 0.33 ms.)  Each thread meets the same elements of every
+// row, so the weights' gradients are sums of its own, kept in shared memory
+// backward; the weights come out of L1, where the rows do not stay.  The grid
+// is the resident blocks only.  Measured, in shares of a copy's rate: 16384 x
+// 4096 with an fp32 residual 178 us (82 %), 524288 rows of 128 with a gate 85
+// us (73 %), backward of 8192 x 4096 143 us (58 %; issue slots half used: three
+// sums over the block a pair of rows, with one block of 16 warps an SM and
+// nothing to run under them).
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -891,15 +892,8 @@ cudaError_t fwd_launch(const NormArgs& a, const Shape& s, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Lets a kernel take shared memory beyond 48 KB.  The limit belongs to the
-// kernel on its device, not to a call, so every call sets the same one: with
-// its own size, a call of another host thread could lower it again before this
-// one's launch.
-constexpr int kMostShared = 226 * 1024;  // of the 227 KB a block may have; the sums take half a KB
-template <typename K>
-cudaError_t allow_shared(K kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-}
+// What these kernels may take: their sums have half a KB of static memory.
+constexpr int kMostShared = kBlockShared - 1024;
 
 // Shared memory of the backward for wide rows; 0 where it does not take them:
 // rows of 64 to 512 whole vectors in whole warps, a gate with a sigmoid, and
@@ -935,7 +929,7 @@ cudaError_t bwd_launch(const NormArgs& a, const Shape& s, int sms, float* part,
   const int per = s.block / s.tpr;
   const int bytes = per * 3 * ((a.width + 3) & ~3) * (int)sizeof(float);
   cudaError_t e = cudaSuccess;
-  if (bytes > 47 * 1024) e = allow_shared(k);  // the static part comes on top
+  if (bytes > 47 * 1024) e = allow_shared(k, kMostShared);  // the static part comes on top
   if (e != cudaSuccess) return e;
   int64_t blocks = resident_blocks(k, s.block, sms, bytes);
   const int64_t most = bwd_blocks(a, s, sms);
@@ -957,7 +951,7 @@ cudaError_t pair_launch(const NormArgs& a, const PairShape& s, int sms, float* p
                                    : norm_bwd_pair_kernel<IO, RT, VEC, 2, false>)
                            : (silu ? norm_bwd_pair_kernel<IO, RT, VEC, 1, true>
                                    : norm_bwd_pair_kernel<IO, RT, VEC, 1, false>);
-  cudaError_t e = allow_shared(k);
+  cudaError_t e = allow_shared(k, kMostShared);
   if (e != cudaSuccess) return e;
   const int64_t need = (a.tokens * a.heads + kPairRows - 1) / kPairRows;
   int64_t blocks = resident_blocks(k, s.threads, sms, s.bytes);

@@ -3,6 +3,7 @@
 // kernel uses, so the operand encodings can be checked in isolation against a
 // library matmul.
 #include "../../include/kda.h"
+#include "kda_common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace kda {
@@ -100,9 +101,7 @@ extern "C" KDA_API kda_status kda_selftest_umma(int a_mn, int b_mn, int N,
   const size_t a_bytes = a_mn ? 2 * panel_rows * 128 : (K / 64) * 128 * 128;
   const size_t b_bytes = b_mn ? (N / 64) * panel_rows * 128 : (K / 64) * N * 128;
   const size_t smem = 1024 + ((a_bytes + 1023) & ~size_t(1023)) + b_bytes + 64;
-  cudaError_t e = cudaFuncSetAttribute(
-      kda::umma_probe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      (int)smem);
+  cudaError_t e = kda::allow_shared(kda::umma_probe_kernel);
   if (e == cudaSuccess) {
     kda::umma_probe_kernel<<<1, 128, smem, stream>>>(
         a_mn, b_mn, N, K, panel_rows, static_cast<const __nv_bfloat16*>(A),

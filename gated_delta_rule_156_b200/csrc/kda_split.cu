@@ -575,12 +575,6 @@ cudaError_t launch_fix_tc(const SplitWs& w, __nv_bfloat16* out,
                     : launch_fix_tc_t<128, 128>(w, out, a, g, grid, flag, stream);
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
-}
-
 // A non-blocking stream per device for the transition run, created on first
 // use and kept for the life of the process.
 cudaError_t side_stream(cudaStream_t* out) {
@@ -606,7 +600,7 @@ template <typename IO, int RM, int RN>
 cudaError_t launch_fix_t(const SplitWs& w, IO* out, const ChunkArgs& a,
                          const SplitGeom& g, dim3 grid, cudaStream_t stream) {
   const size_t smem = 4 * (size_t)a.dk * ((16 * RM + 4) + (16 * RN + 4));
-  cudaError_t e = set_smem(split_fix_kernel<IO, RM, RN>, smem);
+  cudaError_t e = allow_shared(split_fix_kernel<IO, RM, RN>);
   if (e != cudaSuccess) return e;
   split_fix_kernel<IO, RM, RN><<<grid, kThreads, smem, stream>>>(
       w, out, a.T, g.Ls, g.k, a.H, a.dk, a.dv);
@@ -708,7 +702,7 @@ cudaError_t run_split(const ChunkArgs& a, const SplitGeom& g, void* workspace,
   // (3) scan, (4) correction
   const int dk = a.dk, dv = a.dv, H = a.H, C = a.chunk;
   const size_t sms = 4 * ((size_t)dk * kScanTp + (size_t)dk * (dk + 1));
-  if ((e = set_smem(split_scan_kernel, sms)) != cudaSuccess) return e;
+  if ((e = allow_shared(split_scan_kernel)) != cudaSuccess) return e;
   split_scan_kernel<<<dim3(H, dv / kScanTile), kThreads, sms, stream>>>(
       w, a.final_state, g.k, H, dk, dv, fix_on_tensor_cores(a) ? 1 : 0);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -536,12 +536,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
-}
-
 // Which stages run: all four (the forward), or the pieces the backward pass
 // wraps around its own per-chunk preparation (the plan and the cumulative
 // log-decay first, the state pass after W and U are in place).
@@ -577,7 +571,7 @@ cudaError_t run(const ChunkArgs& a, void* workspace, cudaStream_t stream,
 
     const size_t sm2 = 4 * ((size_t)2 * C * (dk + 1) + (size_t)C * dv +
                             2 * 64 * ws::kFS + 1024 + C + 2 * dk);
-    if ((e = set_smem(intra_kernel<IO>, sm2)) != cudaSuccess) return e;
+    if ((e = allow_shared(intra_kernel<IO>)) != cudaSuccess) return e;
     intra_kernel<IO><<<grid, kThreads, sm2, stream>>>(
         k, v, a.beta, w.g, w.w, w.u, w.kh, cu, w.chunk_off, a.n_seqs, a.T, H,
         dk, dv, C);
@@ -589,12 +583,12 @@ cudaError_t run(const ChunkArgs& a, void* workspace, cudaStream_t stream,
                             (size_t)C * tp + dk);
     const dim3 sgrid(a.n_seqs, H, dv / tile);
     if (tile == 64) {
-      if ((e = set_smem(state_kernel<64>, sm3)) != cudaSuccess) return e;
+      if ((e = allow_shared(state_kernel<64>)) != cudaSuccess) return e;
       state_kernel<64><<<sgrid, kThreads, sm3, stream>>>(
           w.g, w.w, w.kh, w.u, w.s, a.initial_state, a.final_state, cu,
           w.chunk_off, a.n_seqs, a.T, H, dk, dv, C);
     } else {
-      if ((e = set_smem(state_kernel<32>, sm3)) != cudaSuccess) return e;
+      if ((e = allow_shared(state_kernel<32>)) != cudaSuccess) return e;
       state_kernel<32><<<sgrid, kThreads, sm3, stream>>>(
           w.g, w.w, w.kh, w.u, w.s, a.initial_state, a.final_state, cu,
           w.chunk_off, a.n_seqs, a.T, H, dk, dv, C);
@@ -605,7 +599,7 @@ cudaError_t run(const ChunkArgs& a, void* workspace, cudaStream_t stream,
   if (nch > 0 && part == Part::kAll) {
     const size_t sm4 = 4 * (2 * (size_t)C * (dk + 1) + (size_t)C * C +
                             (size_t)dk * kDvTile + (size_t)C * kDvTile + dk);
-    if ((e = set_smem(output_kernel<IO>, sm4)) != cudaSuccess) return e;
+    if ((e = allow_shared(output_kernel<IO>)) != cudaSuccess) return e;
     output_kernel<IO><<<dim3((unsigned)nch, H, dv / kDvTile), kThreads, sm4,
                         stream>>>(q, k, w.g, w.u, w.s, out, cu, w.chunk_off,
                                   a.n_seqs, a.T, H, dk, dv, C);
