@@ -971,8 +971,9 @@ def block_norm_fwd(x, post_weight=None, gate=None, residual=None, scale=None,
         out = residual + scale p;  normed = rms(out) pre_weight
 
     x, gate [..., width] (bf16 or fp32; the norms are over the last dim;
-    slices of a projection's output will do, [..., heads, width] with dense
-    tokens or rows at one stride), residual the
+    slices of a projection's output will do: rows at one stride, or tokens
+    [..., heads, width] at one stride with dense heads, and x and gate in the
+    same of these two forms unless one of them is contiguous), residual the
     same shape in x's dtype or fp32, weights and scale [width] fp32,
     ``gate_act`` "sigmoid", "silu" or "none".  ``out`` may be the residual
     itself.  Returns (out in the residual's dtype, normed in x's or None).

@@ -183,3 +183,25 @@ def test_sizes_beyond_the_abi_fields_are_refused():
         shape, _ = K._norm_shape(fake(big, 3, dtype=bf), None, None, None,
                                  None, None, bf, "none", False, 1e-6)
         assert shape.tokens == big and shape.width == 3
+
+
+def test_norm_strides():
+    # rows at one stride, or tokens at one stride with dense heads; a
+    # contiguous tensor goes with either, the two forms not with each other
+    with FakeTensorMode():
+        def fake(*shape):
+            return torch.empty(shape, device="cuda")
+
+        def strides(x, gate):
+            s, _ = K._norm_shape(x, None, gate, None, None, None,
+                                 torch.float32, "silu", False, 1e-6)
+            return s.tokens, s.heads, s.x_stride, s.gate_stride
+        dense, rows = fake(5, 4, 32), fake(5, 4, 48)[..., :32]
+        heads = fake(5, 3, 4, 32)[:, 1]
+        assert strides(dense, rows) == (20, 1, 0, 48)
+        assert strides(rows, rows) == (20, 1, 48, 48)
+        assert strides(dense, heads) == (5, 4, 0, 384)
+        assert strides(heads, dense) == (5, 4, 384, 0)
+        for x, gate in ((rows, heads), (heads, rows)):
+            with pytest.raises(ValueError, match="dense"):
+                strides(x, gate)
